@@ -63,9 +63,15 @@ typedef enum dsa_dtype {
     DSA_F32 = 0,               /* IEEE binary32 */
     DSA_BF16 = 1,              /* bfloat16      */
     /* The FP8 latent cache layout of dsa_latent_row_bytes (656-byte rows at
-     * the V3.2 sizes).  Accepted only by dsa_decode_step(_noalloc) as the
-     * kv_cache type; q_mla and out are then bf16. */
-    DSA_FP8_LATENT = 2
+     * the V3.2 sizes).  Accepted by dsa_decode_step(_noalloc) as the
+     * kv_cache type (q_mla and out are then bf16) and as the cache_dt of the
+     * calls that take one. */
+    DSA_FP8_LATENT = 2,
+    /* The 4-bit latent cache layout of dsa_latent_q4_row_bytes (416-byte rows
+     * at the V3.2 sizes).  Accepted by dsa_decode_step(_noalloc) as the
+     * kv_cache type (q_mla and out are then bf16) and as the cache_dt of the
+     * calls that take one. */
+    DSA_Q4_LATENT = 3
 } dsa_dtype;
 
 /* act_quant's scale_fmt: a plain fp32 scale, or ue8m0 (a bare power of two). */
@@ -309,6 +315,111 @@ dsa_status dsa_sparse_mla_attn(const void *q, const void *kv_cache, int64_t t_ma
                                dsa_stream_t stream);
 
 /*
+ * The 4-bit latent cache (the pages have no counterpart: the FP8 row's idea at
+ * half the width).  Row layout, rows of a multiple of 16 bytes (416 at the V3.2
+ * sizes):
+ *   [dc/2 code bytes | dr bf16 rotary values | dc/32 bf16 scales | zeros]
+ * The latent part is quantised in groups of 32: s = bf16_rn(max(amax, 1e-4) / 7),
+ * n = nearest integer to x / s (ties to even, -7..7), code n + 8; the value a
+ * code stands for is bf16_rn(n * s).  In each little-endian 32-bit word of eight
+ * codes value 2i is nibble i and value 2i + 1 nibble i + 4.  The rotary part is
+ * rounded to bf16.  Same shapes as the FP8 rows.  Latents must be finite.
+ */
+int64_t dsa_latent_q4_row_bytes(int dc, int dr);
+
+/*
+ * From the projection's output to cached latent rows in one pass (MLA.forward:
+ * kv_norm of the kv_lora_rank part, apply_rotary_emb of k_pe, the cache write).
+ * For every token (b, s), with c the first dc elements of its vector and p the
+ * last dr:
+ *   c' = c * (mean(c^2) + eps)^-1/2 * norm_w      (norm_w NULL: c' = c)
+ *   p' = p rotated by rope_cs[s]                  (rope_cs NULL: p' = p)
+ * in fp32, then one rounding into row start_pos + s of the cache: bf16, the FP8
+ * row (dsa_latent_quant's rounding) or the 4-bit row.  interleaved != 0 pairs
+ * elements (2j, 2j + 1) as (re, im), 0 pairs (j, j + dr/2).
+ *
+ *   kv       vector (b, s) at kv + b * batch_stride + s * token_stride (strides
+ *            in elements of x_dtype, F32 or BF16; both multiples of 16 bytes,
+ *            at least dc + dr; a stride of an axis of one is unused)
+ *   norm_w   [dc] fp32 or NULL, eps >= 0      rope_cs  [S, dr/2, 2] fp32 or NULL
+ *   cache    [B, t_max, row]  cache_dt = DSA_BF16, DSA_FP8_LATENT or DSA_Q4_LATENT
+ * kv, norm_w, rope_cs and cache 16-byte aligned.  Shapes as dsa_latent_quant.
+ * Rows other than start_pos .. start_pos + S - 1 are left as they were.
+ */
+dsa_status dsa_latent_prologue(const void *kv, dsa_dtype x_dtype, int64_t batch_stride,
+                               int64_t token_stride, int B, int S, int dc, int dr,
+                               const float *norm_w, float eps, const float *rope_cs,
+                               int interleaved, int64_t start_pos, int64_t t_max, void *cache,
+                               dsa_dtype cache_dt, dsa_stream_t stream);
+
+/*
+ * Read latent rows back: out[b, j, :] = the values that row idx[b, j] (idx NULL:
+ * row start_pos + j) of cache [B, t_max, row] stands for, dc + dr of them, each
+ * a bf16 number (code times scale rounded to bf16), stored as bf16 or fp32.
+ * idx [B, n] int32; an index < 0 gives a row of zeros, one >= t_max too and
+ * records DSA_ERR_DEVICE; start_pos is not used with idx.
+ * cache and out 16-byte aligned; cache_dt and shapes as dsa_latent_prologue.
+ */
+dsa_status dsa_latent_read(const void *cache, dsa_dtype cache_dt, int64_t t_max,
+                           const int32_t *idx, int64_t start_pos, int B, int64_t n, int dc, int dr,
+                           void *out, dsa_dtype out_dtype, dsa_stream_t stream);
+
+/*
+ * Sparse latent attention (as dsa_sparse_mla_attn, bf16) over the 4-bit latent
+ * cache kv_q4 [B, t_max, dsa_latent_q4_row_bytes(dc, dr)], 16-byte aligned.
+ *   q    [B,S,Hq,dc+dr] bf16 (16-byte aligned), idx [B,S,k] int32 (-1 = empty)
+ *   out  [B,S,Hq,dc] bf16 (16-byte aligned), lse [B,S,Hq] fp32 or NULL
+ * 1 <= Hq <= 1024; shapes as dsa_latent_quant.  Each query row's selection is
+ * masked as in dsa_sparse_mla_attn (-1 and indices > start_pos + s are skipped;
+ * a row with nothing left gives out = 0, lse = -inf).
+ * Workspace: dsa_sparse_mla_attn_q4_workspace_size bytes (16-byte aligned).
+ */
+size_t dsa_sparse_mla_attn_q4_workspace_size(int B, int S, int Hq, int dc, int dr, int k);
+dsa_status dsa_sparse_mla_attn_q4(const void *q, const uint8_t *kv_q4, int64_t t_max,
+                                  const int32_t *idx, int B, int S, int Hq, int dc, int dr, int k,
+                                  int64_t start_pos, float sm_scale, void *out, float *lse,
+                                  void *workspace, size_t workspace_bytes, dsa_stream_t stream);
+
+/*
+ * Selection by blocks: the indexer scores one key per block of `block` tokens
+ * instead of one per token, and attention reads the selected blocks whole.
+ * The three steps are dsa_block_keys, then dsa_index_scores_csa and
+ * dsa_topk_select_csa over the block keys (compress = block), then
+ * dsa_block_mla_attn over the selected block ids.
+ *
+ * dsa_block_keys: the keys of the blocks that the tokens start_pos ..
+ * start_pos + S - 1 finish (block e is the tokens [e block, (e + 1) block)).  A
+ * block's key is the mean of its tokens' decoded keys (code * scale) in fp32,
+ * quantised as dsa_indexer_quant quantises a rotated vector.
+ *   k_cache [B,t_max,D] e4m3, k_scale [B,t_max] fp32: the indexer's key cache,
+ *           the new tokens' keys already appended
+ *   blk_cache [B,n_max,D] e4m3, blk_scale [B,n_max] fp32: entry e is written for
+ *           every finished block, nothing else; (start_pos + S) / block <= n_max
+ * D 64 or 128; k_cache and blk_cache 16-byte aligned.
+ */
+dsa_status dsa_block_keys(const uint8_t *k_cache, const float *k_scale, int64_t t_max, int B,
+                          int64_t start_pos, int64_t S, int D, int block, uint8_t *blk_cache,
+                          float *blk_scale, int64_t n_max, dsa_stream_t stream);
+
+/*
+ * Latent attention over selected blocks: the query at position i = start_pos + s
+ * attends to every token of the blocks listed in blk[b,s,:] and to its own
+ * unfinished block, the tokens [(i + 1) / block * block, i].  A listed block
+ * counts when it is finished, 0 <= e < (i + 1) / block; other entries (-1, the
+ * unfinished block, a block ahead of the query) are skipped.  Listed blocks must
+ * be distinct.  Formulas, shapes, outputs and empty rows as
+ * dsa_sparse_mla_attn_q4.
+ *   kv_cache [B,t_max,row] in format cache_dt (DSA_BF16, DSA_FP8_LATENT or
+ *            DSA_Q4_LATENT), 16-byte aligned;  blk [B,S,kb] int32
+ */
+size_t dsa_block_mla_attn_workspace_size(int B, int S, int Hq, int dc, int dr, int kb, int block);
+dsa_status dsa_block_mla_attn(const void *q, const void *kv_cache, dsa_dtype cache_dt,
+                              int64_t t_max, const int32_t *blk, int B, int S, int Hq, int dc,
+                              int dr, int kb, int block, int64_t start_pos, float sm_scale,
+                              void *out, float *lse, void *workspace, size_t workspace_bytes,
+                              dsa_stream_t stream);
+
+/*
  * One DSA decode step for B sequences that each see T tokens (end_pos = T,
  * the new token at position T-1; no mask, as seqlen == 1):
  *   1. rotate + quantise the new token's indexer queries and key; append the
@@ -324,7 +435,8 @@ dsa_status dsa_sparse_mla_attn(const void *q, const void *kv_cache, int64_t t_ma
  *   lse [B,Hq] fp32 or NULL
  * dt = DSA_FP8_LATENT: kv_cache is the FP8 latent cache [B, t_max,
  * dsa_latent_row_bytes(dc, dr)] (16-byte aligned), attended as
- * dsa_sparse_mla_attn_fp8 does; q_mla and out are bf16.
+ * dsa_sparse_mla_attn_fp8 does; q_mla and out are bf16.  dt = DSA_Q4_LATENT:
+ * likewise the 4-bit latent cache, attended as dsa_sparse_mla_attn_q4 does.
  */
 size_t dsa_decode_step_workspace_size(int B, int H, int D, int64_t T, int index_topk, int Hq,
                                       int dc, int dr, dsa_dtype dt);

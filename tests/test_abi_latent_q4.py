@@ -1,0 +1,151 @@
+"""Host-side argument checks of the latent-cache and block entry points: bad
+calls are refused before anything is launched (no GPU needed)."""
+import ctypes
+
+import pytest
+
+NULL = None
+FAKE = ctypes.c_void_p(1 << 20)        # aligned, never dereferenced: checks fail first
+ODD = ctypes.c_void_p((1 << 20) + 4)
+F32, BF16, FP8, Q4 = 0, 1, 2, 3
+OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 6
+
+
+@pytest.fixture(scope="module")
+def dsa():
+    import __graft_entry__
+    __graft_entry__._builder().build()
+    import top_kv_selection_b200 as m
+    return m
+
+
+def test_row_bytes(dsa):
+    assert dsa.dsa_latent_q4_row_bytes(512, 64) == 416
+    for dc in (128, 256, 384, 512):
+        for dr in range(0, 65, 8):
+            rb = dsa.dsa_latent_q4_row_bytes(dc, dr)
+            assert rb % 16 == 0 and 0 <= rb - (dc // 2 + 2 * dr + dc // 16) < 16
+            assert rb != dsa.dsa_latent_row_bytes(dc, dr)      # the binding tells them apart
+
+
+def prologue(L, **kw):
+    a = dict(kv=FAKE, dt=BF16, bs=8 * 576, ts=576, B=2, S=8, dc=512, dr=64, w=FAKE, eps=1e-6, cs=FAKE,
+             il=1, sp=0, t_max=8, cache=FAKE, fmt=Q4)
+    a.update(kw)
+    return L.dsa_latent_prologue(a["kv"], a["dt"], a["bs"], a["ts"], a["B"], a["S"], a["dc"], a["dr"], a["w"],
+                                 a["eps"], a["cs"], a["il"], a["sp"], a["t_max"], a["cache"], a["fmt"], NULL)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dc=500), UNSUPPORTED), (dict(dr=72), UNSUPPORTED), (dict(dr=4), UNSUPPORTED),
+    (dict(dc=640, ts=704), UNSUPPORTED),
+    (dict(dt=2), INVALID), (dict(fmt=F32), INVALID), (dict(fmt=4), INVALID),
+    (dict(kv=NULL), INVALID), (dict(cache=NULL), INVALID), (dict(kv=ODD), INVALID), (dict(cache=ODD), INVALID),
+    (dict(w=ODD), INVALID), (dict(cs=ODD), INVALID),
+    (dict(sp=1), INVALID),                                     # row 8 past the cache
+    (dict(sp=-1), INVALID), (dict(B=-1), INVALID), (dict(S=-1), INVALID),
+    (dict(ts=568), INVALID),                                   # tokens would overlap
+    (dict(ts=580), INVALID), (dict(bs=8 * 576 + 4), INVALID),  # not multiples of 16 bytes
+    (dict(dt=F32, ts=578), INVALID),
+    (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID),
+    (dict(B=0, kv=NULL, cache=NULL), OK), (dict(S=0, kv=NULL, cache=NULL), OK),
+])
+def test_prologue_checks(dsa, kw, status):
+    assert prologue(dsa._lib, **kw) == status
+
+
+def read(L, **kw):
+    a = dict(cache=FAKE, fmt=Q4, t_max=100, idx=NULL, sp=0, B=2, n=100, dc=512, dr=64, out=FAKE, dt=BF16)
+    a.update(kw)
+    return L.dsa_latent_read(a["cache"], a["fmt"], a["t_max"], a["idx"], a["sp"], a["B"], a["n"], a["dc"],
+                             a["dr"], a["out"], a["dt"], NULL)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dc=96), UNSUPPORTED), (dict(dr=65), UNSUPPORTED), (dict(fmt=F32), INVALID), (dict(dt=Q4), INVALID),
+    (dict(sp=1), INVALID), (dict(sp=-1), INVALID), (dict(n=-1), INVALID), (dict(B=-1), INVALID),
+    (dict(cache=NULL), INVALID), (dict(out=NULL), INVALID), (dict(out=ODD), INVALID), (dict(cache=ODD), INVALID),
+    (dict(idx=ctypes.c_void_p((1 << 20) + 2)), INVALID),
+    (dict(n=0, cache=NULL, out=NULL), OK), (dict(B=0, cache=NULL, out=NULL), OK),
+])
+def test_read_checks(dsa, kw, status):
+    assert read(dsa._lib, **kw) == status
+
+
+def keys(L, **kw):
+    a = dict(k=FAKE, ks=FAKE, t_max=128, B=2, sp=0, S=128, D=128, m=64, bk=FAKE, bs=FAKE, n_max=2)
+    a.update(kw)
+    return L.dsa_block_keys(a["k"], a["ks"], a["t_max"], a["B"], a["sp"], a["S"], a["D"], a["m"], a["bk"],
+                            a["bs"], a["n_max"], NULL)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(D=96), UNSUPPORTED), (dict(m=0), INVALID), (dict(n_max=1), INVALID), (dict(sp=1), INVALID),
+    (dict(sp=-1), INVALID), (dict(k=NULL), INVALID), (dict(bk=ODD), INVALID), (dict(k=ODD), INVALID),
+    (dict(B=0, k=NULL), OK),
+    (dict(S=63, k=NULL), OK),                                  # no block is finished: nothing to write
+    (dict(sp=64, S=0, k=NULL), OK),
+])
+def test_block_keys_checks(dsa, kw, status):
+    assert keys(dsa._lib, **kw) == status
+
+
+def attn(dsa, blocks, **kw):
+    L = dsa._lib
+    a = dict(q=FAKE, kv=FAKE, fmt=Q4, t_max=4096, sel=FAKE, B=1, S=1, Hq=128, dc=512, dr=64, k=2048, m=64,
+             sp=4095, out=FAKE, lse=FAKE, ws=FAKE, wsb=1 << 30)
+    if blocks:
+        a["k"] = 32
+    a.update(kw)
+    head = (a["q"], a["kv"]) + ((a["fmt"],) if blocks else ())
+    mid = (a["t_max"], a["sel"], a["B"], a["S"], a["Hq"], a["dc"], a["dr"], a["k"])
+    mid += (a["m"],) if blocks else ()
+    fn = L.dsa_block_mla_attn if blocks else L.dsa_sparse_mla_attn_q4
+    return fn(*head, *mid, a["sp"], 0.04, a["out"], a["lse"], a["ws"], a["wsb"], NULL)
+
+
+@pytest.mark.parametrize("blocks", [False, True])
+@pytest.mark.parametrize("kw,status", [
+    (dict(dc=500), UNSUPPORTED), (dict(dr=72), UNSUPPORTED), (dict(Hq=1025), UNSUPPORTED),
+    (dict(sp=4096), INVALID), (dict(sp=-1), INVALID), (dict(k=0), INVALID), (dict(B=-1), INVALID),
+    (dict(q=ODD), INVALID), (dict(kv=ODD), INVALID), (dict(out=ODD), INVALID), (dict(q=NULL), INVALID),
+    (dict(sel=NULL), INVALID), (dict(out=NULL), INVALID), (dict(lse=ctypes.c_void_p((1 << 20) + 2)), INVALID),
+    (dict(t_max=1 << 32), INVALID),
+    (dict(B=1 << 20, S=1 << 12, sp=0), UNSUPPORTED),
+    (dict(B=0, q=NULL), OK), (dict(S=0, q=NULL), OK), (dict(Hq=0, q=NULL), OK),
+])
+def test_attention_checks(dsa, blocks, kw, status):
+    assert attn(dsa, blocks, **kw) == status
+
+
+def test_block_attention_checks(dsa):
+    assert attn(dsa, True, m=0) == INVALID
+    assert attn(dsa, True, fmt=F32) == INVALID
+    assert attn(dsa, True, k=1 << 20, m=1 << 20) == UNSUPPORTED
+    assert attn(dsa, True, m=(1 << 20) + 1) == UNSUPPORTED
+
+
+def test_workspace_checks(dsa):
+    L = dsa._lib
+    need = L.dsa_sparse_mla_attn_q4_workspace_size(1, 1, 128, 512, 64, 2048)
+    if need:
+        assert attn(dsa, False, wsb=need - 1) == WORKSPACE
+        assert attn(dsa, False, ws=NULL) == WORKSPACE
+        assert attn(dsa, False, ws=ODD) == WORKSPACE
+    assert L.dsa_sparse_mla_attn_q4_workspace_size(1, 1, 128, 500, 64, 2048) == 0
+    assert L.dsa_block_mla_attn_workspace_size(1, 1, 128, 512, 64, 32, 0) == 0
+    assert L.dsa_sparse_mla_attn_q4_workspace_size(0, 1, 128, 512, 64, 2048) == 0
+
+
+def test_decode_step_takes_the_4_bit_cache(dsa):
+    L = dsa._lib
+    need = L.dsa_decode_step_workspace_size(8, 64, 128, 131072, 2048, 128, 512, 64, Q4)
+    assert need >= 8 * 131072 * 4
+
+    def call(dt=Q4, dc=512, ws_bytes=need, Hq=128):
+        return L.dsa_decode_step(FAKE, FAKE, FAKE, FAKE, FAKE, 131072, FAKE, FAKE, 8, 64, 128, Hq, dc, 64,
+                                 131072, 2048, 0.088, 0.041, dt, FAKE, FAKE, NULL, FAKE, ws_bytes, NULL)
+    assert call(dt=4) == INVALID
+    assert call(dc=96) == UNSUPPORTED                 # a bf16 shape, not a 4-bit one
+    assert call(Hq=1025) == UNSUPPORTED
+    assert call(ws_bytes=need - 1) == WORKSPACE

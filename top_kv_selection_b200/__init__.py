@@ -25,7 +25,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_CUDA = 0, 1, 2, 3
 DSA_ERR_TIMEOUT, DSA_ERR_DEVICE, DSA_ERR_WORKSPACE = 4, 5, 6
-DSA_F32, DSA_BF16, DSA_FP8_LATENT = 0, 1, 2
+DSA_F32, DSA_BF16, DSA_FP8_LATENT, DSA_Q4_LATENT = 0, 1, 2, 3
 DSA_SCALE_F32, DSA_SCALE_UE8M0 = 0, 1
 DSA_NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -57,6 +57,17 @@ _SIGNATURES = {
     "dsa_sparse_mla_attn_workspace_size": ([_i32, _i32, _i32, _i32, _i32, _i32, _i32], _sz),
     "dsa_sparse_mla_attn": ([_P, _P, _i64, _P, _i32, _i32, _i32, _i32, _i32, _i32, _i64, _f32,
                              _i32, _P, _P, _P, _sz, _P], _i32),
+    "dsa_latent_q4_row_bytes": ([_i32, _i32], _i64),
+    "dsa_latent_prologue": ([_P, _i32, _i64, _i64, _i32, _i32, _i32, _i32, _P, _f32, _P, _i32, _i64,
+                             _i64, _P, _i32, _P], _i32),
+    "dsa_latent_read": ([_P, _i32, _i64, _P, _i64, _i32, _i64, _i32, _i32, _P, _i32, _P], _i32),
+    "dsa_sparse_mla_attn_q4_workspace_size": ([_i32, _i32, _i32, _i32, _i32, _i32], _sz),
+    "dsa_sparse_mla_attn_q4": ([_P, _P, _i64, _P, _i32, _i32, _i32, _i32, _i32, _i32, _i64, _f32,
+                                _P, _P, _P, _sz, _P], _i32),
+    "dsa_block_keys": ([_P, _P, _i64, _i32, _i64, _i64, _i32, _i32, _P, _P, _i64, _P], _i32),
+    "dsa_block_mla_attn_workspace_size": ([_i32, _i32, _i32, _i32, _i32, _i32, _i32], _sz),
+    "dsa_block_mla_attn": ([_P, _P, _i32, _i64, _P, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i64,
+                            _f32, _P, _P, _P, _sz, _P], _i32),
     "dsa_decode_step_workspace_size": ([_i32, _i32, _i32, _i64, _i32, _i32, _i32, _i32, _i32],
                                        _sz),
     "dsa_decode_step": ([_P, _P, _P, _P, _P, _i64, _P, _P, _i32, _i32, _i32, _i32, _i32, _i32,
@@ -116,9 +127,31 @@ def _dtype(t: torch.Tensor) -> int:
     raise ValueError(f"unsupported dtype {t.dtype}")
 
 
-def _kv_dtype(kv_cache: torch.Tensor, q_mla: torch.Tensor) -> int:
-    """The decode step's cache type: uint8 rows are the FP8 latent cache."""
-    return DSA_FP8_LATENT if kv_cache.dtype == torch.uint8 else _dtype(q_mla)
+def _kv_dtype(kv_cache: torch.Tensor, q_mla: torch.Tensor, dc: int) -> int:
+    """The decode step's cache type: uint8 rows are the 4-bit latent cache when they
+    have its width, else the FP8 latent cache (no shape has equal widths)."""
+    if kv_cache.dtype != torch.uint8:
+        return _dtype(q_mla)
+    q4 = _lib.dsa_latent_q4_row_bytes(dc, q_mla.shape[-1] - dc)
+    return DSA_Q4_LATENT if kv_cache.shape[-1] == q4 else DSA_FP8_LATENT
+
+
+def _check_rows(cache: torch.Tensor, cache_dt: int, dc: int, dr: int) -> None:
+    """The cache [B, t_max, row] has rows of its format."""
+    if cache_dt == DSA_BF16:
+        ok = cache.dtype == torch.bfloat16 and cache.shape[-1] == dc + dr
+    else:
+        row = (_lib.dsa_latent_q4_row_bytes if cache_dt == DSA_Q4_LATENT
+               else _lib.dsa_latent_row_bytes)(dc, dr)
+        ok = cache.dtype == torch.uint8 and cache.shape[-1] == row
+    if cache.dim() != 3 or not ok:
+        raise ValueError(f"the cache [B, t_max, row] {tuple(cache.shape)} {cache.dtype} does not "
+                         f"have the rows of its format at dc = {dc}, dr = {dr}")
+
+
+def _check_tensor(name: str, t: torch.Tensor | None, shape: tuple, dtype: torch.dtype) -> None:
+    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+        raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype}, not {tuple(shape)} {dtype}")
 
 
 def dsa_get_device_error(stream=None) -> int:
@@ -286,6 +319,116 @@ def dsa_sparse_mla_attn(q: torch.Tensor, kv_cache: torch.Tensor, idx: torch.Tens
         sm_scale, _dtype(q), _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)))
 
 
+def dsa_latent_q4_row_bytes(dc: int, dr: int) -> int:
+    return int(_lib.dsa_latent_q4_row_bytes(dc, dr))
+
+
+def dsa_latent_prologue(kv: torch.Tensor, norm_w: torch.Tensor | None, eps: float,
+                        rope_cs: torch.Tensor | None, interleaved: bool, start_pos: int,
+                        cache: torch.Tensor, cache_dt: int, dc: int, stream=None) -> None:
+    """kv [B,S,dc+dr] fp32 or bf16 (the last axis contiguous, any other strides that are
+    multiples of 16 bytes): RMS norm of the first dc elements (norm_w [dc] fp32, or None),
+    rotary embedding of the last dr (rope_cs [S, dr/2, 2] fp32, or None), appended at
+    start_pos to cache [B, t_max, row] in format cache_dt."""
+    B, S, dqk = kv.shape
+    dr = dqk - dc
+    if not kv.is_cuda:
+        raise ValueError("libdsa takes CUDA tensors only")
+    if dqk > 1 and kv.stride(-1) != 1:
+        raise ValueError("the last axis of kv must be contiguous")
+    _check_rows(cache, cache_dt, dc, dr)
+    if cache.shape[0] != B:
+        raise ValueError(f"kv has {B} sequences, the cache {cache.shape[0]}")
+    _check_tensor("norm_w", norm_w, (dc,), torch.float32)
+    _check_tensor("rope_cs", rope_cs, (S, dr // 2, 2), torch.float32)
+    _check("dsa_latent_prologue", _lib.dsa_latent_prologue(
+        ctypes.c_void_p(kv.data_ptr()), _dtype(kv), kv.stride(0), kv.stride(1), B, S, dc, dr,
+        _ptr(norm_w), eps, _ptr(rope_cs), 1 if interleaved else 0, start_pos, cache.shape[1],
+        _ptr(cache), cache_dt, _stream(stream)))
+
+
+def dsa_latent_read(cache: torch.Tensor, cache_dt: int, start_pos: int, out: torch.Tensor,
+                    dc: int, idx: torch.Tensor | None = None, stream=None) -> None:
+    """out [B,n,dc+dr] (bf16 or fp32) = the values of rows start_pos .. start_pos + n - 1 of
+    cache [B, t_max, row], or of the rows idx [B,n] int32 (zeros for an index < 0)."""
+    B, n, dqk = out.shape
+    _check_rows(cache, cache_dt, dc, dqk - dc)
+    if cache.shape[0] != B:
+        raise ValueError(f"out has {B} sequences, the cache {cache.shape[0]}")
+    _check_tensor("idx", idx, (B, n), torch.int32)
+    _check("dsa_latent_read", _lib.dsa_latent_read(
+        _ptr(cache), cache_dt, cache.shape[1], _ptr(idx), start_pos, B, n, dc, dqk - dc, _ptr(out),
+        _dtype(out), _stream(stream)))
+
+
+def _check_attn(q: torch.Tensor, cache: torch.Tensor, cache_dt: int, sel: torch.Tensor, dc: int,
+                out: torch.Tensor, lse: torch.Tensor | None) -> None:
+    B, S, Hq, dqk = q.shape
+    _check_rows(cache, cache_dt, dc, dqk - dc)
+    if q.dtype != torch.bfloat16 or cache.shape[0] != B:
+        raise ValueError("q must be bf16, the cache hold q's sequences")
+    _check_tensor("the selection", sel, (B, S, sel.shape[-1]), torch.int32)
+    _check_tensor("out", out, (B, S, Hq, dc), torch.bfloat16)
+    _check_tensor("lse", lse, (B, S, Hq), torch.float32)
+
+
+def dsa_sparse_mla_attn_q4_workspace_size(B: int, S: int, Hq: int, dc: int, dr: int,
+                                          k: int) -> int:
+    return int(_lib.dsa_sparse_mla_attn_q4_workspace_size(B, S, Hq, dc, dr, k))
+
+
+def dsa_sparse_mla_attn_q4(q: torch.Tensor, kv_q4: torch.Tensor, idx: torch.Tensor,
+                           start_pos: int, sm_scale: float, dc: int, out: torch.Tensor,
+                           lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                           stream=None) -> None:
+    """q [B,S,Hq,dc+dr] bf16, kv_q4 [B,t_max,row_bytes] uint8, idx [B,S,k] int32 ->
+    out [B,S,Hq,dc] bf16, lse [B,S,Hq] fp32."""
+    B, S, Hq, dqk = q.shape
+    _check_attn(q, kv_q4, DSA_Q4_LATENT, idx, dc, out, lse)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check("dsa_sparse_mla_attn_q4", _lib.dsa_sparse_mla_attn_q4(
+        _ptr(q), _ptr(kv_q4), kv_q4.shape[1], _ptr(idx), B, S, Hq, dc, dqk - dc, idx.shape[-1],
+        start_pos, sm_scale, _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def dsa_block_keys(k_cache: torch.Tensor, k_scale: torch.Tensor, start_pos: int, S: int,
+                   block: int, blk_cache: torch.Tensor, blk_scale: torch.Tensor,
+                   stream=None) -> None:
+    """The keys of the blocks (of `block` tokens) that tokens start_pos .. start_pos + S - 1
+    finish, from k_cache [B,t_max,D] uint8 / k_scale [B,t_max], into blk_cache [B,n_max,D]
+    uint8 / blk_scale [B,n_max]."""
+    B, t_max, D = k_cache.shape
+    n_max = blk_cache.shape[1]
+    _check_tensor("k_cache", k_cache, (B, t_max, D), torch.uint8)
+    _check_tensor("k_scale", k_scale, (B, t_max), torch.float32)
+    _check_tensor("blk_cache", blk_cache, (B, n_max, D), torch.uint8)
+    _check_tensor("blk_scale", blk_scale, (B, n_max), torch.float32)
+    _check("dsa_block_keys", _lib.dsa_block_keys(
+        _ptr(k_cache), _ptr(k_scale), t_max, B, start_pos, S, D, block, _ptr(blk_cache),
+        _ptr(blk_scale), n_max, _stream(stream)))
+
+
+def dsa_block_mla_attn_workspace_size(B: int, S: int, Hq: int, dc: int, dr: int, kb: int,
+                                      block: int) -> int:
+    return int(_lib.dsa_block_mla_attn_workspace_size(B, S, Hq, dc, dr, kb, block))
+
+
+def dsa_block_mla_attn(q: torch.Tensor, kv_cache: torch.Tensor, cache_dt: int, blk: torch.Tensor,
+                       block: int, start_pos: int, sm_scale: float, dc: int, out: torch.Tensor,
+                       lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                       stream=None) -> None:
+    """q [B,S,Hq,dc+dr] bf16, kv_cache [B,t_max,row] in format cache_dt, blk [B,S,kb] int32
+    ids of finished blocks (-1 = empty) -> out [B,S,Hq,dc] bf16, lse [B,S,Hq] fp32; each
+    query's own unfinished block is attended too."""
+    B, S, Hq, dqk = q.shape
+    _check_attn(q, kv_cache, cache_dt, blk, dc, out, lse)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check("dsa_block_mla_attn", _lib.dsa_block_mla_attn(
+        _ptr(q), _ptr(kv_cache), cache_dt, kv_cache.shape[1], _ptr(blk), B, S, Hq, dc, dqk - dc,
+        blk.shape[-1], block, start_pos, sm_scale, _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes,
+        _stream(stream)))
+
+
 def dsa_decode_step_workspace_size(B: int, H: int, D: int, T: int, index_topk: int, Hq: int,
                                    dc: int, dr: int, dt: int) -> int:
     return _lib.dsa_decode_step_workspace_size(B, H, D, T, index_topk, Hq, dc, dr, dt)
@@ -307,7 +450,7 @@ def dsa_decode_step(q_idx: torch.Tensor, w: torch.Tensor, k_new: torch.Tensor,
     _check("dsa_decode_step", _lib.dsa_decode_step(
         _ptr(q_idx), _ptr(w), _ptr(k_new), _ptr(k_cache), _ptr(k_scale), t_max, _ptr(kv_cache),
         _ptr(q_mla), B, H, D, Hq, dc, dqk - dc, T, index_topk, softmax_scale, sm_scale,
-        _kv_dtype(kv_cache, q_mla), _ptr(idx), _ptr(out), _ptr(lse), _ptr(workspace),
+        _kv_dtype(kv_cache, q_mla, dc), _ptr(idx), _ptr(out), _ptr(lse), _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
@@ -326,4 +469,4 @@ def dsa_decode_step_noalloc(q_idx: torch.Tensor, w: torch.Tensor, k_new: torch.T
     _check("dsa_decode_step_noalloc", _lib.dsa_decode_step_noalloc(
         _ptr(q_idx), _ptr(w), _ptr(k_new), _ptr(k_cache), _ptr(k_scale), t_max, _ptr(kv_cache),
         _ptr(q_mla), B, H, D, Hq, dc, dqk - dc, T, index_topk, softmax_scale, sm_scale,
-        _kv_dtype(kv_cache, q_mla), _ptr(idx), _ptr(out), _ptr(lse), _stream(stream)))
+        _kv_dtype(kv_cache, q_mla, dc), _ptr(idx), _ptr(out), _ptr(lse), _stream(stream)))

@@ -177,5 +177,13 @@ dsa_status launch_sparse_mla(const void *q, const void *kv, int64_t t_max, const
                              int B, int S, int Hq, int dc, int dr, int k, int64_t start_pos,
                              float sm_scale, dsa_dtype dt, void *out, float *lse, void *ws,
                              cudaStream_t stream);
+// Attention over selected positions (block = 0) or selected blocks of `block`
+// tokens, rows in format fmt (DSA_BF16, DSA_FP8_LATENT or DSA_Q4_LATENT)
+// (latent_attn.cu).
+size_t latent_attn_workspace_bytes(int B, int S, int Hq, int dc, int dr, int n_sel, int block);
+dsa_status launch_latent_attn(const void *q, const void *kv, dsa_dtype fmt, int64_t t_max,
+                              const int32_t *sel, int n_sel, int block, int B, int S, int Hq,
+                              int dc, int dr, int64_t start_pos, float sm_scale, void *out,
+                              float *lse, void *ws, cudaStream_t stream);
 
 }  // namespace dsa

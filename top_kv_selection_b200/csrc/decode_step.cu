@@ -38,8 +38,9 @@ DecodeWs carve(void *base, int B, int H, int D, int64_t T, int index_topk, int H
     w.hist = reinterpret_cast<uint32_t *>(
         take((size_t)B * w.hist_chunks * kHistBins * sizeof(uint32_t)));
     const int K = (int64_t)index_topk < T ? index_topk : (int)T;
-    w.attn_ws = take(dt == DSA_FP8_LATENT ? sparse_mla_fp8_workspace_bytes(B, 1, Hq, dc, dr, K)
-                                          : sparse_mla_workspace_bytes(B, 1, Hq, dc, dr, K, dt));
+    w.attn_ws = take(dt == DSA_FP8_LATENT  ? sparse_mla_fp8_workspace_bytes(B, 1, Hq, dc, dr, K)
+                     : dt == DSA_Q4_LATENT ? latent_attn_workspace_bytes(B, 1, Hq, dc, dr, K, 0)
+                                           : sparse_mla_workspace_bytes(B, 1, Hq, dc, dr, K, dt));
     w.total = off;
     return w;
 }
@@ -62,12 +63,15 @@ extern "C" dsa_status dsa_decode_step(const float *q_idx, const float *w, const 
                                       size_t workspace_bytes, dsa_stream_t stream) {
     if (B < 0 || H < 1 || Hq < 1 || index_topk < 1 || T < 1 || T > t_max || T > INT32_MAX)
         return DSA_ERR_INVALID_ARG;
-    if (dt != DSA_F32 && dt != DSA_BF16 && dt != DSA_FP8_LATENT) return DSA_ERR_INVALID_ARG;
+    if (dt != DSA_F32 && dt != DSA_BF16 && dt != DSA_FP8_LATENT && dt != DSA_Q4_LATENT)
+        return DSA_ERR_INVALID_ARG;
     if (D != 64 && D != 128) return DSA_ERR_UNSUPPORTED;
     if (H > 256) return DSA_ERR_UNSUPPORTED;
     if (dc == 0 || dc % 32 != 0 || dc > 512 || dr < 0 || dr % 8 != 0 || dc + dr > 576)
         return DSA_ERR_UNSUPPORTED;
-    if (dt == DSA_FP8_LATENT && !dsa::latent_fp8_shape_ok(dc, dr)) return DSA_ERR_UNSUPPORTED;
+    if ((dt == DSA_FP8_LATENT || dt == DSA_Q4_LATENT) && !dsa::latent_fp8_shape_ok(dc, dr))
+        return DSA_ERR_UNSUPPORTED;
+    if (dt == DSA_Q4_LATENT && Hq > 1024) return DSA_ERR_UNSUPPORTED;
     if (B == 0) return DSA_OK;
     if (!q_idx || !w || !k_new || !k_cache || !k_scale || !kv_cache || !q_mla || !idx || !out)
         return DSA_ERR_INVALID_ARG;
@@ -93,6 +97,9 @@ extern "C" dsa_status dsa_decode_step(const float *q_idx, const float *w, const 
         return dsa::launch_sparse_mla_fp8(q_mla, static_cast<const uint8_t *>(kv_cache), t_max,
                                           idx, B, 1, Hq, dc, dr, K, T - 1, sm_scale, out, lse,
                                           ws.attn_ws, s);
+    if (dt == DSA_Q4_LATENT)
+        return dsa::launch_latent_attn(q_mla, kv_cache, dt, t_max, idx, K, 0, B, 1, Hq, dc, dr,
+                                       T - 1, sm_scale, out, lse, ws.attn_ws, s);
     return dsa::launch_sparse_mla(q_mla, kv_cache, t_max, idx, B, 1, Hq, dc, dr, K, T - 1,
                                   sm_scale, dt, out, lse, ws.attn_ws, s);
 }
