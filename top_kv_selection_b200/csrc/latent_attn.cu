@@ -10,128 +10,693 @@
 // query's own unfinished block, the last (i + 1) mod m positions, is added as
 // slot 0.
 //
-// One warp per (query row, head): lane l holds the latent values
-// [8 l, 8 l + 8) and [8 l + 256, 8 l + 264) and the rotary pair l of the query
-// and of each row, and walks the selection with an online softmax.
+// Tensor-core form, transposed: the keys are the MMA's M, the heads its N.
+//   S^T[key, head] = C Q^T       M = 128 slots, N = 16, 32 or 64 heads, K = dc + dr
+//   O^T[dc, head] += C^T P^T     M = 128 columns of dc at a time, K = 128 slots
+// so the output of a CTA's heads takes dc / 128 x N TMEM columns (256 for 64
+// heads of 512 columns) and the logits have room beside it: one CTA walks any
+// number of 128-slot tiles of its query row with an online softmax, without
+// leaving TMEM, and few heads cost few columns.  (With the heads as M, 512
+// output columns fill TMEM and each tile's result has to leave it.)
+//
+// One CTA = (query row, group of up to 64 heads, share of the row's slots).
+// Sixteen work warps and one MMA warp:
+//   - the tile's rows are decoded to bf16 in 64-column chunks, 128B-swizzled
+//     K-major tiles that serve as the logits' A operand and, read MN-major, as
+//     the value mix's.  Quantised rows are loaded into registers one tile
+//     ahead (four threads a row) and decoded as the value mix of the tile
+//     before frees each pair of chunks; bf16 rows are copied by cp.async, their
+//     lines requested into L2 one tile ahead;
+//   - softmax: thread = (slot, quarter of the heads), the running maximum of each
+//     head is a reference kept until a logit passes it by more than 8 (2^8 in
+//     the weights, which bf16 and the fp32 sums hold at full precision); only
+//     then are the maxima of the tile reduced and the output rescaled.  Sums
+//     stay per thread in fp32 and are reduced once at the end; the weights are
+//     rounded to bf16 as MMA operands (the sums take them unrounded);
+//   - splits of a row (when there are fewer rows than SMs) leave fp32 partials
+//     that a second kernel merges.
 #include "latent_rows.cuh"
+#include "tc_ptx.cuh"
 
 namespace dsa {
 namespace {
 
-constexpr int kHeadsPerCta = 8;
+constexpr int kTile = 128;                      // slots per tile (the MMA M of the logits)
+constexpr int kRegion = kTile * 128;            // one 64-column chunk of a tile: 16 KB
+constexpr int kWork = 512;
+constexpr int kThreads = kWork + 32;
+constexpr int kMaxHeads = 64;                   // heads per CTA
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 8.f;                   // how far (log2) a logit may pass the reference
+
+struct AttnArgs {
+    const __nv_bfloat16 *q;     // [rows, Hq, dc + dr]
+    const uint8_t *kv;          // [B, t_max, row]
+    const int32_t *sel;         // [rows, n_sel] positions or block ids
+    __nv_bfloat16 *out;
+    float *lse;
+    float *part_o;              // [units][heads][dc] (splits > 1)
+    float2 *part_ml;            // [units][heads] (reference, sum)
+    int64_t t_max, start_pos, row_bytes;
+    int n_sel, block, slots;    // block = 0: the list holds positions
+    int S, Hq, dc, dr;
+    int groups, splits, split_slots;
+    float scale_log2;           // sm_scale * log2(e)
+    int *err;
+};
+
+// Control block behind the tiles and the query.
+struct alignas(16) Control {
+    float red[4][kMaxHeads];    // per TMEM lane quarter: maxima, later sums
+    float ref[kMaxHeads];       // the heads' references (-inf: no logit seen)
+    float sub[kMaxHeads];       // the same, 0 instead of -inf: what is subtracted
+    float fac[kMaxHeads];       // rescaling of this tile; at the end 1 / sum
+    int32_t list[kTile];        // the tile's rows (bf16 gather)
+    uint64_t full[5];           // chunk pair m (4: the rotary chunk) is in shared memory
+    uint64_t q_full, s_done, p_full, mma_fin;
+    uint64_t o_done[4];         // value mix of dc columns [128 m, 128 m + 128) is complete
+    uint32_t tmem;
+    int abort;
+    int last;                   // last slot of the share that counts
+};
+
+size_t smem_bytes(int dc, int nh) {
+    return 1024 + (size_t)(dc / 64 + 1) * (kRegion + nh * 128) + sizeof(Control);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t src_bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+// Arrives on `bar` once every cp.async this thread issued so far has landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+// Loads that stay behind griddepcontrol.wait (volatile, coherent).
+__device__ __forceinline__ uint4 ld_v4(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint32_t ld_b32(const void *p) {
+    uint32_t v;
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint16_t ld_u16(const void *p) {
+    uint16_t v;
+    asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    return v;
+}
+// 16 bytes that are 16-byte aligned (wide) or 4-byte aligned
+__device__ __forceinline__ uint4 ld_piece(const uint8_t *p, bool wide) {
+    if (wide) return ld_v4(p);
+    return make_uint4(ld_b32(p), ld_b32(p + 4), ld_b32(p + 8), ld_b32(p + 12));
+}
+// 2^x by the SFU (relative error about 2^-22; 2^-inf = +0).
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// a softmax thread's columns
+__device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t (&v)[8]) { tc::tmem_ld8(taddr, v); }
+__device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t (&v)[16]) { tc::tmem_ld16(taddr, v); }
+__device__ __forceinline__ float warp_max_redux(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// The cache row of a selection slot of query row `row`, or -1.  Slot 0's block
+// is the query's unfinished one; `limit` < t_max, so every position that is
+// not ahead of the query lies in the cache.
+__device__ __forceinline__ int32_t slot_row(const AttnArgs &a, const int32_t *list, int slot, int limit, int done) {
+    if (slot >= a.slots) return -1;
+    int32_t t;
+    if (a.block == 0) {
+        t = (int32_t)ld_b32(list + slot);
+    } else {
+        const int e = (int)((unsigned)slot / (unsigned)a.block);
+        const int32_t b = e == 0 ? done : (int32_t)ld_b32(list + e - 1);
+        if (b < 0 || (e > 0 && b >= done)) return -1;
+        const int64_t p = (int64_t)b * a.block + (slot - e * a.block);
+        t = p > limit ? -1 : (int32_t)p;
+    }
+    return t < 0 || t > limit ? -1 : t;
+}
+
+// What a thread holds of its row of the next tile: of each chunk pair m the
+// half h & 1 of chunk 2m + (h >> 1), h = the thread's quarter of the row, and a
+// quarter of the rotary part.
+template <int F> struct RawRow;
+template <> struct RawRow<DSA_Q4_LATENT> {
+    uint4 code[4];
+    uint16_t scale[4];
+    uint4 rope[2];
+};
+template <> struct RawRow<DSA_FP8_LATENT> {
+    uint4 code[4][2];
+    float scale[4];
+    uint4 rope[2];
+};
+template <> struct RawRow<DSA_BF16> {};
 
 template <int F>
-__global__ void __launch_bounds__(32 * kHeadsPerCta)
-latent_attn_kernel(const __nv_bfloat16 *__restrict__ q, const uint8_t *__restrict__ kv, int64_t t_max,
-                   const int32_t *__restrict__ sel, int n_sel, int block, int S, int Hq, int dc, int dr,
-                   int64_t start_pos, float sm_scale, __nv_bfloat16 *__restrict__ out,
-                   float *__restrict__ lse, int *err) {
-    const int lane = threadIdx.x & 31;
-    const int head = blockIdx.y * kHeadsPerCta + (threadIdx.x >> 5);
-    const int64_t row = blockIdx.x, b = row / S, s = row - b * S;
-    if (head >= Hq) return;
-    const int64_t limit = start_pos + s;
-    const int64_t rb = latent_fmt_row_bytes(F, dc, dr);
-    const int chunks = dc / 8;
-    const __nv_bfloat16 *qh = q + (row * Hq + head) * (dc + dr);
-    float qv[2][8], o[2][8], q0 = 0.f, q1 = 0.f;
+__device__ __forceinline__ void load_raw(RawRow<F> &r, const AttnArgs &a, int64_t rbase, int32_t t, int h) {
+    const uint8_t *row = a.kv + (rbase + (t < 0 ? 0 : t)) * a.row_bytes;
+    const bool v = t >= 0;
+    const bool wide = F == DSA_Q4_LATENT || (a.row_bytes & 15) == 0;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    const int mt = a.dc / 128;
 #pragma unroll
-    for (int u = 0; u < 2; u++)
-#pragma unroll
-        for (int e = 0; e < 8; e++) {
-            const int d = 8 * (lane + 32 * u) + e;
-            qv[u][e] = d < dc ? __bfloat162float(qh[d]) : 0.f;
-            o[u][e] = 0.f;
-        }
-    if (lane < dr / 2) {
-        q0 = __bfloat162float(qh[dc + 2 * lane]);
-        q1 = __bfloat162float(qh[dc + 2 * lane + 1]);
-    }
-    float m = -INFINITY, l = 0.f;
-    const int32_t *list = sel + row * n_sel;
-    // block = 0: the list holds positions
-    const int64_t done = block ? (limit + 1) / block : 0;
-    const int64_t slots = block ? (int64_t)(n_sel + 1) * block : n_sel;
-    for (int64_t j = 0; j < slots; j++) {
-        int64_t t;
-        if (block) {
-            const int64_t e = j / block;
-            const int64_t blk = e == 0 ? done : list[e - 1];
-            if (blk < 0 || (e > 0 && blk >= done)) continue;
-            t = blk * block + (j - e * block);
+    for (int m = 0; m < 4; m++) {
+        if constexpr (F == DSA_Q4_LATENT) {
+            r.code[m] = m < mt && v ? ld_v4(row + 64 * m + 16 * h) : zero;
+            r.scale[m] = m < mt && v ? ld_u16(row + latent_q4_scales_at(a.dc, a.dr) + 8 * m + 2 * h) : (uint16_t)0;
         } else {
-            t = list[j];
-        }
-        if (t < 0 || t > limit) continue;
-        if (t >= t_max) {
-            if (lane == 0) record_error(err, DSA_ERR_DEVICE);
-            continue;
-        }
-        const uint8_t *c = kv + (b * t_max + t) * rb;
-        float cv[2][8], part = 0.f;
 #pragma unroll
-        for (int u = 0; u < 2; u++) {
-            const uint4 w = lane + 32 * u < chunks ? latent_chunk8<F>(c, dc, dr, lane + 32 * u)
-                                                   : make_uint4(0, 0, 0, 0);
-            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+            for (int p = 0; p < 2; p++)
+                r.code[m][p] = m < mt && v ? ld_piece(row + 128 * m + 32 * h + 16 * (p ^ (h >> 1)), wide) : zero;
+            r.scale[m] = m < mt && v ? __uint_as_float(ld_b32(row + a.dc + 4 * m)) : 0.f;
+        }
+    }
+    const uint8_t *pe = row + latent_rope_at<F>(a.dc);
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const float2 f = bf16x2_to_f32(ws[e]);
-                cv[u][2 * e] = f.x;
-                cv[u][2 * e + 1] = f.y;
+    for (int p = 0; p < 2; p++) {
+        const int piece = 2 * h + p;                       // values [8 piece, 8 piece + 8)
+        r.rope[p] = v && 8 * piece < a.dr ? ld_piece(pe + 16 * piece, wide) : zero;
+    }
+}
+
+// Decodes the thread's share of chunk pair m into the tile.  The threads of
+// the upper chunk (h >> 1 = 1) store their four 16-byte units in the order 2,
+// 3, 0, 1: with the swizzle, the two rows x four threads that store together
+// then touch all banks once.
+template <int F>
+__device__ __forceinline__ void store_pair(const RawRow<F> &r, int m, uint32_t tile, int h, int j) {
+    const uint32_t dst = tile + (2 * m + (h >> 1)) * kRegion + j * 128;
+    const int sw = j & 7, up = h >> 1, u0 = 4 * (h & 1);
+    if constexpr (F == DSA_Q4_LATENT) {
+        const __nv_bfloat16 s1 = __ushort_as_bfloat16(r.scale[m]);
+        const __nv_bfloat162 s = __halves2bfloat162(s1, s1);
+        const uint4 c = r.code[m];
+        const uint32_t w[4] = {up ? c.z : c.x, up ? c.w : c.y, up ? c.x : c.z, up ? c.y : c.w};
+#pragma unroll
+        for (int u = 0; u < 4; u++)
+            st_shared_v4(dst + (((u0 + (u ^ (2 * up))) ^ sw) << 4), q4_decode8(w[u], s));
+    } else {
+#pragma unroll
+        for (int p = 0; p < 2; p++) {
+            const int u = u0 + 2 * (p ^ up);
+            const uint4 w = r.code[m][p];
+            st_shared_v4(dst + ((u ^ sw) << 4), fp8_decode8(w.x, w.y, r.scale[m]));
+            st_shared_v4(dst + (((u + 1) ^ sw) << 4), fp8_decode8(w.z, w.w, r.scale[m]));
+        }
+    }
+}
+
+template <int F, int NH>
+__global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs a) {
+    constexpr int kCols = NH == 16 ? 8 : NH / 4;           // heads per softmax thread
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int nc = a.dc / 64, mt = a.dc / 128;             // latent chunks, dc tiles
+    uint8_t *qs = sm + (nc + 1) * kRegion;
+    Control &ctl = *reinterpret_cast<Control *>(qs + (nc + 1) * NH * 128);
+    volatile int *abort = &ctl.abort;
+    const uint32_t tile = tc::smem_u32(sm), qbase = tc::smem_u32(qs);
+    const uint32_t pbase = tile + nc * kRegion;            // P takes the rotary chunk's place
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    // TMEM: the logits, then the output tiles
+    const uint32_t ncols = NH * (mt + 1) <= 32 ? 32 : NH * (mt + 1) <= 64 ? 64 : NH * (mt + 1) <= 128 ? 128
+                           : NH * (mt + 1) <= 256 ? 256 : 512;
+    if (warp == kWork / 32) {
+        if (lane == 0) {
+            for (int i = 0; i < 5; i++) tc::mbar_init(&ctl.full[i], kWork);
+            tc::mbar_init(&ctl.q_full, kWork);
+            tc::mbar_init(&ctl.s_done, 1);
+            tc::mbar_init(&ctl.p_full, kWork);
+            tc::mbar_init(&ctl.mma_fin, 1);
+            for (int i = 0; i < 4; i++) tc::mbar_init(&ctl.o_done[i], 1);
+            ctl.abort = 0;
+            ctl.last = -1;
+            tc::fence_mbar_init();
+        }
+        __syncwarp();
+        tc::tmem_alloc(&ctl.tmem, ncols);
+        tc::tmem_relinquish();
+    }
+    if (threadIdx.x < NH) {
+        ctl.ref[threadIdx.x] = -INFINITY;
+        ctl.sub[threadIdx.x] = 0.f;
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = ctl.tmem;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // every global read comes after this (a no-op without a programmatic launch)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    // blockIdx.x = (row * groups + g) * splits + sp
+    const int sp = (int)(blockIdx.x % (unsigned)a.splits);
+    const unsigned rg = blockIdx.x / (unsigned)a.splits;
+    const int g = (int)(rg % (unsigned)a.groups);
+    const int64_t row = rg / (unsigned)a.groups;
+    const int64_t b = row / a.S;
+    const int limit = (int)(a.start_pos + (row - b * a.S));
+    const int done = a.block ? (limit + 1) / a.block : 0;
+    const int32_t *list = a.sel + row * a.n_sel;
+    const int lo = sp * a.split_slots;
+    const int hi = lo + a.split_slots < a.slots ? lo + a.split_slots : a.slots;
+    const int h0 = g * kMaxHeads;                          // first head
+    const int heads = a.Hq - h0 < NH ? a.Hq - h0 : NH;
+    const int64_t rbase = b * a.t_max;
+
+    if (warp < kWork / 32) {
+        const int t = threadIdx.x;
+        const int j = t >> 2, h = t & 3;                   // gather: row of the tile, quarter of it
+        // softmax: TMEM lane quarter, quarter of the heads (16 heads: the first
+        // two take eight each)
+        const int q4 = warp & 3, c = warp >> 2;
+        const bool active = c * kCols < NH;
+        const int key = q4 * 32 + lane;
+        const uint32_t lane_addr = (uint32_t)(q4 * 32) << 16;
+        bool ok = true;
+
+        // the query, as nc + 1 K-major blocks of 64 columns (absent heads and
+        // columns are zero-filled)
+        {
+            const int dqk = a.dc + a.dr;
+            const __nv_bfloat16 *q = a.q + (row * a.Hq + h0) * dqk;
+            for (int f = t; f < (nc + 1) * NH * 8; f += kWork) {
+                const int p = f & 7, head = (f >> 3) % NH, blk = (f >> 3) / NH;
+                const bool v = head < heads && blk * 64 + p * 8 < dqk;
+                cp_async16(qbase + blk * NH * 128 + head * 128 + ((p ^ (head & 7)) << 4),
+                           q + (v ? head * dqk + blk * 64 + p * 8 : 0), v ? 16u : 0u);
+            }
+            cp_async_arrive(&ctl.q_full);
+        }
+        int32_t trow = slot_row(a, list, lo + j < hi ? lo + j : a.slots, limit, done);
+        bool kv_ok = slot_row(a, list, lo + key < hi ? lo + key : a.slots, limit, done) >= 0;
+        RawRow<F> raw;
+        if constexpr (F != DSA_BF16) load_raw<F>(raw, a, rbase, trow, h);
+        // the share's last slot that counts bounds the walk
+        {
+            int last = -1;
+            for (int s = lo + t; s < hi; s += kWork)
+                if (slot_row(a, list, s, limit, done) >= 0) last = s;
+            last = __reduce_max_sync(0xffffffffu, last);
+            if (lane == 0 && last >= 0) atomicMax(&ctl.last, last);
+        }
+        tc::named_barrier(2, kThreads);
+        const int tiles = ctl.last < lo ? 0 : (ctl.last - lo) / kTile + 1;
+        float lsum[kCols];
+#pragma unroll
+        for (int e = 0; e < kCols; e++) lsum[e] = 0.f;
+
+        for (int i = 0; i < tiles; i++) {
+            const uint32_t ph = i & 1, prev = ph ^ 1;
+            // ------------------------------------------------ the tile's rows
+            if constexpr (F == DSA_BF16) {
+                if (h == 0) ctl.list[j] = trow;
+                tc::named_barrier(1, kWork);
+                for (int m = 0; m <= mt; m++) {
+                    // chunk pair m is free once the last tile's value mix m is
+                    // complete; the rotary chunk (and P) once all of it is
+                    if (i > 0 && m < mt && !tc::mbar_wait(&ctl.o_done[m], prev, a.err, abort)) ok = false;
+                    for (int k = 2 * m; k < (m < mt ? 2 * m + 2 : 2 * m + 1); k++) {
+#pragma unroll
+                        for (int u = 0; u < kTile * 8 / kWork; u++) {
+                            const int f = t + u * kWork, r = f >> 3, p = f & 7;
+                            const int32_t tr = ctl.list[r];
+                            const bool v = tr >= 0 && k * 64 + p * 8 < a.dc + a.dr;
+                            cp_async16(tile + k * kRegion + r * 128 + ((p ^ (r & 7)) << 4),
+                                       a.kv + (rbase + (v ? tr : 0)) * a.row_bytes + (v ? k * 128 + p * 16 : 0),
+                                       v ? 16u : 0u);
+                        }
+                    }
+                    cp_async_arrive(&ctl.full[m < mt ? m : 4]);
+                }
+            } else {
+#pragma unroll
+                for (int m = 0; m < 4; m++) {
+                    if (m >= mt) break;
+                    if (i > 0 && !tc::mbar_wait(&ctl.o_done[m], prev, a.err, abort)) ok = false;
+                    store_pair<F>(raw, m, tile, h, j);
+                    tc::fence_proxy_async_smem();
+                    tc::mbar_arrive(&ctl.full[m]);
+                }
+#pragma unroll
+                for (int p = 0; p < 2; p++)
+                    st_shared_v4(pbase + j * 128 + (((2 * h + p) ^ (j & 7)) << 4), raw.rope[p]);
+                tc::fence_proxy_async_smem();
+                tc::mbar_arrive(&ctl.full[4]);
+            }
+            const bool valid = kv_ok;
+            if (i + 1 < tiles) {
+                const int s0 = lo + (i + 1) * kTile;
+                trow = slot_row(a, list, s0 + j < hi ? s0 + j : a.slots, limit, done);
+                kv_ok = slot_row(a, list, s0 + key < hi ? s0 + key : a.slots, limit, done) >= 0;
+                if constexpr (F == DSA_BF16) {
+                    if (h == 0 && trow >= 0)
+                        tc::prefetch_l2_bulk(a.kv + (rbase + trow) * a.row_bytes, (uint32_t)a.row_bytes);
+                } else {
+                    load_raw<F>(raw, a, rbase, trow, h);
+                }
+            }
+            // ---------------------------------------------------- softmax
+            if (!tc::mbar_wait(&ctl.s_done, ph, a.err, abort)) ok = false;
+            tc::tc_fence_after();
+            float z[kCols];
+            bool over = false;
+            if (active) {
+                uint32_t v[kCols];
+                ld_cols(tmem + lane_addr + c * kCols, v);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < kCols; e++) z[e] = __uint_as_float(v[e]) * a.scale_log2;
             }
 #pragma unroll
-            for (int e = 0; e < 8; e++) part = fmaf(qv[u][e], cv[u][e], part);
+            for (int e = 0; active && e < kCols; e += 4) {
+                const float4 r = *reinterpret_cast<const float4 *>(&ctl.ref[c * kCols + e]);
+                const float rs[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                for (int x = 0; x < 4; x++) over |= z[e + x] > rs[x] + kSlack;
+            }
+            if (tc::named_barrier_any(1, kWork, over && valid)) {
+                // new references: the tile's maxima, per lane quarter and then
+                // over the four
+#pragma unroll
+                for (int e = 0; active && e < kCols; e++) {
+                    const float m = warp_max_redux(valid ? z[e] : -INFINITY);
+                    if (lane == e) ctl.red[q4][c * kCols + e] = m;
+                }
+                tc::named_barrier(1, kWork);
+                if (t < NH) {
+                    const float old = ctl.ref[t];
+                    const float m = fmaxf(fmaxf(fmaxf(ctl.red[0][t], ctl.red[1][t]),
+                                                fmaxf(ctl.red[2][t], ctl.red[3][t])), old);
+                    ctl.fac[t] = old == m ? 1.f : ex2(old - m);
+                    ctl.ref[t] = m;
+                    ctl.sub[t] = m == -INFINITY ? 0.f : m;
+                }
+                tc::named_barrier(1, kWork);
+                if (i > 0 && active) {
+#pragma unroll
+                    for (int e = 0; e < kCols; e++) lsum[e] *= ctl.fac[c * kCols + e];
+                    for (int m = 0; m < mt; m++) {
+#pragma unroll
+                        for (int u = 0; u < kCols / 8; u++) {
+                            const uint32_t col = tmem + lane_addr + NH * (m + 1) + c * kCols + 8 * u;
+                            uint32_t v[8];
+                            tc::tmem_ld8(col, v);
+                            tc::tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 8; e++)
+                                v[e] = __float_as_uint(__uint_as_float(v[e]) * ctl.fac[c * kCols + 8 * u + e]);
+                            tc::tmem_st8(col, v);
+                        }
+                    }
+                    tc::tmem_wait_st();
+                }
+            }
+#pragma unroll
+            for (int u = 0; active && u < kCols / 8; u++) {
+                const float4 s0 = *reinterpret_cast<const float4 *>(&ctl.sub[c * kCols + 8 * u]);
+                const float4 s1 = *reinterpret_cast<const float4 *>(&ctl.sub[c * kCols + 8 * u + 4]);
+                const float sub[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+                uint32_t pk[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const int x = 8 * u + 2 * e;
+                    const float p0 = valid ? ex2(z[x] - sub[2 * e]) : 0.f;
+                    const float p1 = valid ? ex2(z[x + 1] - sub[2 * e + 1]) : 0.f;
+                    lsum[x] += p0;
+                    lsum[x + 1] += p1;
+                    pk[e] = bf16x2_bits(__floats2bfloat162_rn(p0, p1));
+                }
+                st_shared_v4(pbase + key * 128 + (((c * (kCols / 8) + u) ^ (key & 7)) << 4),
+                             make_uint4(pk[0], pk[1], pk[2], pk[3]));
+            }
+            tc::fence_proxy_async_smem();
+            tc::tc_fence_before();
+            tc::mbar_arrive(&ctl.p_full);
         }
-        if (lane < dr / 2) {
-            const float2 f = bf16x2_to_f32(reinterpret_cast<const uint32_t *>(c + latent_rope_at<F>(dc))[lane]);
-            part = fmaf(q0, f.x, fmaf(q1, f.y, part));
+        // -------------------------------------------------------- epilogue
+        if (tiles > 0 && active) {
+#pragma unroll
+            for (int e = 0; e < kCols; e++) {
+                const float s = warp_sum(lsum[e]);
+                if (lane == e) ctl.red[q4][c * kCols + e] = s;
+            }
         }
-        const float z = warp_sum(part) * sm_scale;
-        if (z == -INFINITY) continue;              // weight 0 (and no reference to subtract)
-        const float m_new = fmaxf(m, z);
-        const float corr = m == m_new ? 1.f : expf(m - m_new);
-        const float p = expf(z - m_new);
-        l = fmaf(l, corr, p);
+        tc::named_barrier(1, kWork);
+        const int64_t unit = blockIdx.x;
+        if (t < heads) {
+            const float l = tiles ? (ctl.red[0][t] + ctl.red[1][t]) + (ctl.red[2][t] + ctl.red[3][t]) : 0.f;
+            // (l is NaN where a logit is: it passes through)
+            ctl.fac[t] = l == 0.f ? 0.f : 1.f / l;
+            if (a.splits > 1)
+                a.part_ml[unit * NH + t] = make_float2(l == 0.f ? -INFINITY : ctl.ref[t], l);
+            else if (a.lse)
+                a.lse[row * a.Hq + h0 + t] = l == 0.f ? -INFINITY : (ctl.ref[t] + log2f(l)) * kLn2;
+        }
+        tc::named_barrier(1, kWork);
+        if (tiles == 0) {
+            // nothing selected: zeros (a split's empty partial is its -inf alone)
+            if (a.splits == 1)
+                for (int f = t; f < heads * a.dc / 8; f += kWork)
+                    reinterpret_cast<uint4 *>(a.out + (row * a.Hq + h0) * a.dc)[f] = make_uint4(0, 0, 0, 0);
+            tc::mbar_wait(&ctl.q_full, 0, a.err, abort);
+        } else {
+            const uint32_t ph = (tiles - 1) & 1;
+            for (int m = 0; m < mt; m++) {
+                if (!tc::mbar_wait(&ctl.o_done[m], ph, a.err, abort)) ok = false;
+                tc::tc_fence_after();
+                // thread = (column of dc, quarter of the heads): a warp stores 32
+                // consecutive columns of one head at a time
+                const int col = m * 128 + key;
+                if (active) {
+                    uint32_t v[kCols];
+                    ld_cols(tmem + lane_addr + NH * (m + 1) + c * kCols, v);
+                    tc::tmem_wait_ld();
 #pragma unroll
-        for (int u = 0; u < 2; u++)
-#pragma unroll
-            for (int e = 0; e < 8; e++) o[u][e] = fmaf(o[u][e], corr, p * cv[u][e]);
-        m = m_new;
+                    for (int e = 0; e < kCols; e++) {
+                        const int hd = c * kCols + e;
+                        if (hd >= heads || !ok) continue;
+                        if (a.splits > 1)
+                            a.part_o[(unit * NH + hd) * a.dc + col] = __uint_as_float(v[e]);
+                        else
+                            a.out[(row * a.Hq + h0 + hd) * a.dc + col] =
+                                __float2bfloat16_rn(__uint_as_float(v[e]) * ctl.fac[hd]);
+                    }
+                }
+            }
+        }
+    } else {
+        // ------------------------------------------------------------- MMA
+        tc::named_barrier(2, kThreads);
+        const int tiles = ctl.last < lo ? 0 : (ctl.last - lo) / kTile + 1;
+        if (lane == 0) {
+            const uint32_t id_qk = tc::instr_desc(tc::kFmtBF16, tc::kFmtBF16, 128, NH);
+            const uint32_t id_pv = tc::instr_desc(tc::kFmtBF16, tc::kFmtBF16, 128, NH, true, true);
+            bool ok = tiles > 0 && tc::mbar_wait(&ctl.q_full, 0, a.err, abort);
+            for (int i = 0; ok && i < tiles; i++) {
+                const uint32_t ph = i & 1;
+                for (int m = 0; ok && m <= mt; m++) {
+                    ok = tc::mbar_wait(&ctl.full[m < mt ? m : 4], ph, a.err, abort);
+                    // written through the generic proxy (cp.async or stores)
+                    tc::fence_proxy_async_smem();
+                    tc::tc_fence_after();
+                    for (int k = 2 * m; ok && k < (m < mt ? 2 * m + 2 : 2 * m + 1); k++) {
+                        const int steps = k < nc ? 4 : (a.dr + 15) / 16;
+                        for (int ks = 0; ks < steps; ks++)
+                            tc::mma_f16(tmem, tc::smem_desc(tile + k * kRegion + ks * 32, 1024, tc::kSwizzle128B),
+                                        tc::smem_desc(qbase + k * NH * 128 + ks * 32, 1024, tc::kSwizzle128B),
+                                        id_qk, k > 0 || ks > 0);
+                    }
+                }
+                if (!ok) break;
+                tc::tc_commit(&ctl.s_done);
+                if (!(ok = tc::mbar_wait(&ctl.p_full, ph, a.err, abort))) break;
+                tc::tc_fence_after();
+                // step ks: slots [16 ks, 16 ks + 16) of the chunk pair (A, two
+                // 64-column atoms 16 KB apart) and of P (B), both MN-major
+                for (int m = 0; m < mt; m++) {
+                    for (int ks = 0; ks < kTile / 16; ks++)
+                        tc::mma_f16(tmem + NH * (m + 1),
+                                    tc::smem_desc(tile + 2 * m * kRegion + ks * 2048, 1024, tc::kSwizzle128B, kRegion),
+                                    tc::smem_desc(pbase + ks * 2048, 1024, tc::kSwizzle128B, kRegion), id_pv,
+                                    i > 0 || ks > 0);
+                    tc::tc_commit(&ctl.o_done[m]);
+                }
+            }
+            // every issued MMA completes before TMEM is released
+            tc::tc_commit(&ctl.mma_fin);
+            tc::mbar_wait(&ctl.mma_fin, 0, a.err, abort);
+        }
+        __syncwarp();
     }
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-    __nv_bfloat16 *oh = out + (row * Hq + head) * dc;
-#pragma unroll
-    for (int u = 0; u < 2; u++) {
-        if (lane + 32 * u >= chunks) continue;
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; e++) w[e] = bf16x2_bits(__floats2bfloat162_rn(o[u][2 * e] * inv, o[u][2 * e + 1] * inv));
-        reinterpret_cast<uint4 *>(oh)[lane + 32 * u] = make_uint4(w[0], w[1], w[2], w[3]);
+    tc::tc_fence_before();
+    __syncthreads();
+    if (warp == kWork / 32) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc(tmem, ncols);
     }
-    if (lse && lane == 0) lse[row * Hq + head] = l == 0.f ? -INFINITY : m + logf(l);
+}
+
+// Merges a row's splits: thread = four output columns of one head.
+//   M = max_s ref_s,  out = sum_s 2^(ref_s - M) O_s / sum_s 2^(ref_s - M) l_s
+__global__ void __launch_bounds__(128)
+latent_combine_kernel(const float *part_o, const float2 *part_ml, int splits, int groups, int nh, int Hq, int dc,
+                      __nv_bfloat16 *out, float *lse) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t row = blockIdx.x / (unsigned)Hq;
+    const int head = (int)(blockIdx.x % (unsigned)Hq);
+    const int64_t unit = (row * groups + head / kMaxHeads) * splits;
+    const int hd = head % kMaxHeads;
+    float M = -INFINITY;
+    for (int s = 0; s < splits; s++) M = fmaxf(M, part_ml[(unit + s) * nh + hd].x);
+    float L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = 0; s < splits; s++) {
+        const float2 ml = part_ml[(unit + s) * nh + hd];
+        if (ml.y == 0.f) continue;                         // an empty share wrote no partial
+        const float w = ml.x == M ? 1.f : ex2(ml.x - M);
+        L = fmaf(w, ml.y, L);
+        const float4 o = reinterpret_cast<const float4 *>(part_o + ((unit + s) * nh + hd) * dc)[threadIdx.x];
+        acc.x = fmaf(w, o.x, acc.x);
+        acc.y = fmaf(w, o.y, acc.y);
+        acc.z = fmaf(w, o.z, acc.z);
+        acc.w = fmaf(w, o.w, acc.w);
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    uint2 w;
+    w.x = bf16x2_bits(__floats2bfloat162_rn(acc.x * inv, acc.y * inv));
+    w.y = bf16x2_bits(__floats2bfloat162_rn(acc.z * inv, acc.w * inv));
+    reinterpret_cast<uint2 *>(out + (row * Hq + head) * dc)[threadIdx.x] = w;
+    if (threadIdx.x == 0 && lse) lse[row * Hq + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
+// How a call is cut: heads per CTA, head groups, splits of each row's slots.
+struct Plan {
+    int nh, groups, splits, split_slots;
+    size_t o_bytes, total;
+};
+
+Plan make_plan(int64_t rows, int Hq, int dc, int slots) {
+    Plan p;
+    // the MMA's N: a head count that fits 16 or 32 columns takes that many
+    p.nh = Hq <= 16 ? 16 : Hq <= 32 ? 32 : kMaxHeads;
+    p.groups = (Hq + p.nh - 1) / p.nh;
+    const int64_t units = rows * p.groups;
+    const int tiles = (slots + kTile - 1) / kTile;
+    // one CTA per SM: split a row's tiles over the SMs that are left
+    const int64_t share = units > 0 ? num_sms() / units : 1;
+    int splits = share < 1 ? 1 : share < tiles ? (int)share : tiles;
+    const int per = (tiles + splits - 1) / splits;
+    p.splits = (tiles + per - 1) / per;
+    p.split_slots = per * kTile;
+    p.o_bytes = p.total = 0;
+    if (p.splits > 1) {
+        const size_t n = (size_t)units * p.splits * p.nh;
+        p.o_bytes = align_up(n * dc * sizeof(float), 256);
+        p.total = p.o_bytes + n * sizeof(float2);
+    }
+    return p;
+}
+
+int slots_of(int n_sel, int block) { return block ? (n_sel + 1) * block : n_sel; }
+
+template <int F, int NH>
+dsa_status launch_kernel(const AttnArgs &a, unsigned grid, cudaStream_t st) {
+    const size_t smem = smem_bytes(a.dc, NH);
+    if (cudaFuncSetAttribute(latent_attn_kernel<F, NH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)smem_bytes(512, NH)) != cudaSuccess)
+        return DSA_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    // programmatic: the set-up overlaps the preceding kernel's tail
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, latent_attn_kernel<F, NH>, a) != cudaSuccess) return DSA_ERR_CUDA;
+    return launch_status();
+}
+
+template <int F>
+dsa_status launch_heads(const AttnArgs &a, int nh, unsigned grid, cudaStream_t st) {
+    return nh == 16   ? launch_kernel<F, 16>(a, grid, st)
+           : nh == 32 ? launch_kernel<F, 32>(a, grid, st)
+                      : launch_kernel<F, 64>(a, grid, st);
 }
 
 }  // namespace
 
-size_t latent_attn_workspace_bytes(int B, int S, int Hq, int dc, int dr, int n_sel, int block) { return 0; }
+size_t latent_attn_workspace_bytes(int B, int S, int Hq, int dc, int dr, int n_sel, int block) {
+    (void)dr;
+    return make_plan((int64_t)B * S, Hq, dc, slots_of(n_sel, block)).total;
+}
 
 dsa_status launch_latent_attn(const void *q, const void *kv, dsa_dtype fmt, int64_t t_max, const int32_t *sel,
                               int n_sel, int block, int B, int S, int Hq, int dc, int dr, int64_t start_pos,
                               float sm_scale, void *out, float *lse, void *ws, cudaStream_t st) {
-    const dim3 grid((unsigned)((int64_t)B * S), (unsigned)((Hq + kHeadsPerCta - 1) / kHeadsPerCta));
-    int *err = device_error_word();
-    auto run = [&](auto kernel) {
-        kernel<<<grid, 32 * kHeadsPerCta, 0, st>>>(
-            static_cast<const __nv_bfloat16 *>(q), static_cast<const uint8_t *>(kv), t_max, sel, n_sel, block, S,
-            Hq, dc, dr, start_pos, sm_scale, static_cast<__nv_bfloat16 *>(out), lse, err);
-    };
-    if (fmt == DSA_BF16)
-        run(latent_attn_kernel<DSA_BF16>);
-    else if (fmt == DSA_FP8_LATENT)
-        run(latent_attn_kernel<DSA_FP8_LATENT>);
-    else
-        run(latent_attn_kernel<DSA_Q4_LATENT>);
+    const int64_t rows = (int64_t)B * S;
+    AttnArgs a = {};
+    a.slots = slots_of(n_sel, block);
+    const Plan p = make_plan(rows, Hq, dc, a.slots);
+    a.q = static_cast<const __nv_bfloat16 *>(q);
+    a.kv = static_cast<const uint8_t *>(kv);
+    a.sel = sel;
+    a.out = static_cast<__nv_bfloat16 *>(out);
+    a.lse = lse;
+    a.part_o = static_cast<float *>(ws);
+    a.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(ws) + p.o_bytes);
+    a.t_max = t_max;
+    a.start_pos = start_pos;
+    a.row_bytes = latent_fmt_row_bytes(fmt, dc, dr);
+    a.n_sel = n_sel;
+    a.block = block;
+    a.S = S;
+    a.Hq = Hq;
+    a.dc = dc;
+    a.dr = dr;
+    a.groups = p.groups;
+    a.splits = p.splits;
+    a.split_slots = p.split_slots;
+    a.scale_log2 = sm_scale * kLog2e;
+    a.err = device_error_word();
+    const unsigned grid = (unsigned)(rows * p.groups * p.splits);
+    const dsa_status s = fmt == DSA_BF16         ? launch_heads<DSA_BF16>(a, p.nh, grid, st)
+                         : fmt == DSA_FP8_LATENT ? launch_heads<DSA_FP8_LATENT>(a, p.nh, grid, st)
+                                                 : launch_heads<DSA_Q4_LATENT>(a, p.nh, grid, st);
+    if (s != DSA_OK || p.splits == 1) return s;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(rows * Hq));
+    cfg.blockDim = dim3((unsigned)(dc / 4));
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, latent_combine_kernel, (const float *)a.part_o, (const float2 *)a.part_ml,
+                           p.splits, p.groups, p.nh, Hq, dc, a.out, lse) != cudaSuccess)
+        return DSA_ERR_CUDA;
     return launch_status();
 }
 

@@ -330,6 +330,21 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         : "memory");
 }
 
+// The same with eight columns.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
+                     taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 __device__ __forceinline__ void tmem_wait_st() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -355,12 +370,14 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t smem_addr, uint32_t sbo_b
     return d;
 }
 
-// Instruction descriptor: D fp32, A/B format codes, A K-major, B K-major
-// (b_mn_major = false) or MN-major, N and M.
+// Instruction descriptor: D fp32, A/B format codes, each operand K-major
+// (mn_major = false) or MN-major, N and M.
 __host__ __device__ constexpr uint32_t instr_desc(uint32_t a_fmt, uint32_t b_fmt, int M, int N,
-                                                  bool b_mn_major = false) {
+                                                  bool b_mn_major = false,
+                                                  bool a_mn_major = false) {
     return (1u << 4)                            // D format: F32
            | (a_fmt << 7) | (b_fmt << 10)       // operand formats
+           | ((a_mn_major ? 1u : 0u) << 15)     // A major-ness
            | ((b_mn_major ? 1u : 0u) << 16)     // B major-ness
            | ((uint32_t)(N >> 3) << 17)         // N / 8
            | ((uint32_t)(M >> 4) << 24);        // M / 16
