@@ -20,21 +20,24 @@
 // output columns fill TMEM and each tile's result has to leave it.)
 //
 // One CTA = (query row, group of up to 64 heads, share of the row's slots).
-// Sixteen work warps and one MMA warp:
-//   - the tile's rows are decoded to bf16 in 64-column chunks, 128B-swizzled
-//     K-major tiles that serve as the logits' A operand and, read MN-major, as
-//     the value mix's.  Quantised rows are loaded into registers one tile
-//     ahead (four threads a row) and decoded as the value mix of the tile
-//     before frees each pair of chunks; bf16 rows are copied by cp.async, their
-//     lines requested into L2 one tile ahead;
-//   - softmax: thread = (slot, quarter of the heads), the running maximum of each
-//     head is a reference kept until a logit passes it by more than 8 (2^8 in
-//     the weights, which bf16 and the fp32 sums hold at full precision); only
-//     then are the maxima of the tile reduced and the output rescaled.  Sums
-//     stay per thread in fp32 and are reduced once at the end; the weights are
-//     rounded to bf16 as MMA operands (the sums take them unrounded);
-//   - splits of a row (when there are fewer rows than SMs) leave fp32 partials
-//     that a second kernel merges.
+// Three roles, so that none holds another's registers:
+//   - eight producer warps decode the tile's rows to bf16 in 64-column chunks,
+//     128B-swizzled K-major tiles that serve as the logits' A operand and, read
+//     MN-major, as the value mix's.  Quantised rows are loaded into registers
+//     one tile ahead (two threads a row) and decoded as the value mix of the
+//     tile before frees each pair of chunks; bf16 rows are copied by cp.async,
+//     their lines requested into L2 one tile ahead;
+//   - eight softmax warps: thread = (slot, half of the heads); the running
+//     maximum of each head is a reference kept until a logit passes it by more
+//     than 8 (2^8 in the weights, which bf16 and the fp32 sums hold at full
+//     precision); only then are the tile's maxima reduced and the output
+//     rescaled.  Sums stay per thread in fp32 and are reduced once at the end;
+//     the weights are rounded to bf16 as MMA operands (the sums take them
+//     unrounded).  They also hold the next tile's rotary parts, which go where
+//     the weights were once the value mix has read those;
+//   - one thread issues the MMAs.
+// Splits of a row (when there are fewer rows than SMs) leave fp32 partials that
+// a second kernel merges.
 #include "latent_rows.cuh"
 #include "tc_ptx.cuh"
 
@@ -43,7 +46,8 @@ namespace {
 
 constexpr int kTile = 128;                      // slots per tile (the MMA M of the logits)
 constexpr int kRegion = kTile * 128;            // one 64-column chunk of a tile: 16 KB
-constexpr int kWork = 512;
+constexpr int kSoft = 256, kProd = 256;         // softmax threads, producer threads
+constexpr int kWork = kSoft + kProd;
 constexpr int kThreads = kWork + 32;
 constexpr int kMaxHeads = 64;                   // heads per CTA
 constexpr float kLog2e = 1.4426950408889634f;
@@ -71,8 +75,8 @@ struct alignas(16) Control {
     float red[4][kMaxHeads];    // per TMEM lane quarter: maxima, later sums
     float ref[kMaxHeads];       // the heads' references (-inf: no logit seen)
     float sub[kMaxHeads];       // the same, 0 instead of -inf: what is subtracted
+    float lim[kMaxHeads];       // reference + slack: a logit above it moves the reference
     float fac[kMaxHeads];       // rescaling of this tile; at the end 1 / sum
-    int32_t list[kTile];        // the tile's rows (bf16 gather)
     uint64_t full[5];           // chunk pair m (4: the rotary chunk) is in shared memory
     uint64_t q_full, s_done, p_full, mma_fin;
     uint64_t o_done[4];         // value mix of dc columns [128 m, 128 m + 128) is complete
@@ -105,11 +109,6 @@ __device__ __forceinline__ uint4 ld_v4(const void *p) {
 __device__ __forceinline__ uint32_t ld_b32(const void *p) {
     uint32_t v;
     asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
-    return v;
-}
-__device__ __forceinline__ uint16_t ld_u16(const void *p) {
-    uint16_t v;
-    asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
     return v;
 }
 // 16 bytes that are 16-byte aligned (wide) or 4-byte aligned
@@ -150,19 +149,16 @@ __device__ __forceinline__ int32_t slot_row(const AttnArgs &a, const int32_t *li
     return t < 0 || t > limit ? -1 : t;
 }
 
-// What a thread holds of its row of the next tile: of each chunk pair m the
-// half h & 1 of chunk 2m + (h >> 1), h = the thread's quarter of the row, and a
-// quarter of the rotary part.
+// What a producer holds of its row of the next tile: chunks 2m + h, h = the
+// thread's half of the row's chunk pairs.
 template <int F> struct RawRow;
 template <> struct RawRow<DSA_Q4_LATENT> {
-    uint4 code[4];
-    uint16_t scale[4];
-    uint4 rope[2];
+    uint4 code[4][2];
+    uint32_t scale[4];          // of both pieces
 };
 template <> struct RawRow<DSA_FP8_LATENT> {
-    uint4 code[4][2];
+    uint4 code[4][4];
     float scale[4];
-    uint4 rope[2];
 };
 template <> struct RawRow<DSA_BF16> {};
 
@@ -175,54 +171,79 @@ __device__ __forceinline__ void load_raw(RawRow<F> &r, const AttnArgs &a, int64_
     const int mt = a.dc / 128;
 #pragma unroll
     for (int m = 0; m < 4; m++) {
+        const bool on = v && m < mt;
         if constexpr (F == DSA_Q4_LATENT) {
-            r.code[m] = m < mt && v ? ld_v4(row + 64 * m + 16 * h) : zero;
-            r.scale[m] = m < mt && v ? ld_u16(row + latent_q4_scales_at(a.dc, a.dr) + 8 * m + 2 * h) : (uint16_t)0;
+            // (the half-1 thread takes its two pieces in the other order: with
+            // the swizzle, the four rows x two threads that store together then
+            // touch all banks once)
+            r.code[m][0] = on ? ld_v4(row + 64 * m + 32 * h + 16 * h) : zero;
+            r.code[m][1] = on ? ld_v4(row + 64 * m + 32 * h + 16 * (h ^ 1)) : zero;
+            r.scale[m] = on ? ld_b32(row + latent_q4_scales_at(a.dc, a.dr) + 8 * m + 4 * h) : 0u;
         } else {
 #pragma unroll
-            for (int p = 0; p < 2; p++)
-                r.code[m][p] = m < mt && v ? ld_piece(row + 128 * m + 32 * h + 16 * (p ^ (h >> 1)), wide) : zero;
-            r.scale[m] = m < mt && v ? __uint_as_float(ld_b32(row + a.dc + 4 * m)) : 0.f;
+            for (int p = 0; p < 4; p++)
+                r.code[m][p] = on ? ld_piece(row + 128 * m + 64 * h + 16 * (p ^ (2 * h)), wide) : zero;
+            r.scale[m] = on ? __uint_as_float(ld_b32(row + a.dc + 4 * m)) : 0.f;
         }
-    }
-    const uint8_t *pe = row + latent_rope_at<F>(a.dc);
-#pragma unroll
-    for (int p = 0; p < 2; p++) {
-        const int piece = 2 * h + p;                       // values [8 piece, 8 piece + 8)
-        r.rope[p] = v && 8 * piece < a.dr ? ld_piece(pe + 16 * piece, wide) : zero;
     }
 }
 
-// Decodes the thread's share of chunk pair m into the tile.  The threads of
-// the upper chunk (h >> 1 = 1) store their four 16-byte units in the order 2,
-// 3, 0, 1: with the swizzle, the two rows x four threads that store together
-// then touch all banks once.
+// Decodes the thread's half of chunk pair m into the tile.
 template <int F>
 __device__ __forceinline__ void store_pair(const RawRow<F> &r, int m, uint32_t tile, int h, int j) {
-    const uint32_t dst = tile + (2 * m + (h >> 1)) * kRegion + j * 128;
-    const int sw = j & 7, up = h >> 1, u0 = 4 * (h & 1);
+    const uint32_t dst = tile + (2 * m + h) * kRegion + j * 128;
+    const int sw = j & 7;
     if constexpr (F == DSA_Q4_LATENT) {
-        const __nv_bfloat16 s1 = __ushort_as_bfloat16(r.scale[m]);
-        const __nv_bfloat162 s = __halves2bfloat162(s1, s1);
-        const uint4 c = r.code[m];
-        const uint32_t w[4] = {up ? c.z : c.x, up ? c.w : c.y, up ? c.x : c.z, up ? c.y : c.w};
-#pragma unroll
-        for (int u = 0; u < 4; u++)
-            st_shared_v4(dst + (((u0 + (u ^ (2 * up))) ^ sw) << 4), q4_decode8(w[u], s));
-    } else {
 #pragma unroll
         for (int p = 0; p < 2; p++) {
-            const int u = u0 + 2 * (p ^ up);
-            const uint4 w = r.code[m][p];
-            st_shared_v4(dst + ((u ^ sw) << 4), fp8_decode8(w.x, w.y, r.scale[m]));
-            st_shared_v4(dst + (((u + 1) ^ sw) << 4), fp8_decode8(w.z, w.w, r.scale[m]));
+            const int piece = p ^ h;
+            const __nv_bfloat16 s1 = __ushort_as_bfloat16((uint16_t)(r.scale[m] >> (16 * piece)));
+            const __nv_bfloat162 s = __halves2bfloat162(s1, s1);
+            const uint32_t w[4] = {r.code[m][p].x, r.code[m][p].y, r.code[m][p].z, r.code[m][p].w};
+#pragma unroll
+            for (int u = 0; u < 4; u++) st_shared_v4(dst + (((4 * piece + u) ^ sw) << 4), q4_decode8(w[u], s));
         }
+    } else {
+#pragma unroll
+        for (int p = 0; p < 4; p++) {
+            const int piece = p ^ (2 * h);
+            const uint4 w = r.code[m][p];
+            st_shared_v4(dst + (((2 * piece) ^ sw) << 4), fp8_decode8(w.x, w.y, r.scale[m]));
+            st_shared_v4(dst + (((2 * piece + 1) ^ sw) << 4), fp8_decode8(w.z, w.w, r.scale[m]));
+        }
+    }
+}
+
+// Values [32 c, 32 c + 32) of a row's rotary part (zeros past its width).
+template <int F>
+__device__ __forceinline__ void load_rope(uint4 (&r)[4], const AttnArgs &a, int64_t rbase, int32_t t, int c) {
+    const uint8_t *pe = a.kv + (rbase + (t < 0 ? 0 : t)) * a.row_bytes + latent_rope_at<F>(a.dc) + 64 * c;
+    const bool wide = F != DSA_FP8_LATENT || (a.row_bytes & 15) == 0;
+#pragma unroll
+    for (int p = 0; p < 4; p++)
+        r[p] = t >= 0 && 32 * c + 8 * p < a.dr ? ld_piece(pe + 16 * p, wide) : make_uint4(0, 0, 0, 0);
+}
+
+// Copies 128 bytes of each of the warp's sixteen bf16 rows, from byte `at`, into
+// a chunk (zeros for an empty slot).  Eight lanes copy a row; row r's cache row
+// is held by lane 2 r.
+__device__ __forceinline__ void copy_chunk(const AttnArgs &a, int64_t rbase, int32_t trow, int at, uint32_t chunk,
+                                           int pwarp, int lane) {
+    const int p = lane & 7;
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+        const int r = 4 * u + (lane >> 3), j = 16 * pwarp + r;
+        const int32_t t = __shfl_sync(0xffffffffu, trow, 2 * r);
+        cp_async16(chunk + j * 128 + ((p ^ (j & 7)) << 4), a.kv + (rbase + (t < 0 ? 0 : t)) * a.row_bytes + at + 16 * p,
+                   t < 0 ? 0u : 16u);
     }
 }
 
 template <int F, int NH>
 __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs a) {
-    constexpr int kCols = NH == 16 ? 8 : NH / 4;           // heads per softmax thread
+    constexpr int kCols = NH / 2;                          // heads per softmax thread
+    constexpr int kStep = 8;                               // logits a softmax thread holds at a time
+    constexpr int kOut = NH == 16 ? 8 : NH / 4;            // heads per thread of the epilogue
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int nc = a.dc / 64, mt = a.dc / 128;             // latent chunks, dc tiles
@@ -238,10 +259,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
                            : NH * (mt + 1) <= 256 ? 256 : 512;
     if (warp == kWork / 32) {
         if (lane == 0) {
-            for (int i = 0; i < 5; i++) tc::mbar_init(&ctl.full[i], kWork);
-            tc::mbar_init(&ctl.q_full, kWork);
+            for (int i = 0; i < 4; i++) tc::mbar_init(&ctl.full[i], kProd);
+            tc::mbar_init(&ctl.full[4], kSoft);
+            tc::mbar_init(&ctl.q_full, kProd);
             tc::mbar_init(&ctl.s_done, 1);
-            tc::mbar_init(&ctl.p_full, kWork);
+            tc::mbar_init(&ctl.p_full, kSoft);
             tc::mbar_init(&ctl.mma_fin, 1);
             for (int i = 0; i < 4; i++) tc::mbar_init(&ctl.o_done[i], 1);
             ctl.abort = 0;
@@ -255,6 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
     if (threadIdx.x < NH) {
         ctl.ref[threadIdx.x] = -INFINITY;
         ctl.sub[threadIdx.x] = 0.f;
+        ctl.lim[threadIdx.x] = -INFINITY;
     }
     tc::tc_fence_before();
     __syncthreads();
@@ -279,148 +302,104 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
     const int heads = a.Hq - h0 < NH ? a.Hq - h0 : NH;
     const int64_t rbase = b * a.t_max;
 
-    if (warp < kWork / 32) {
+    // the share's last slot that counts bounds the walk (a share of one tile is
+    // walked as it is)
+    const int32_t count_all = hi - lo <= kTile ? 1 : 0;
+    bool ok = true;
+    int tiles = 1;
+
+    if (warp < kSoft / 32) {
         const int t = threadIdx.x;
-        const int j = t >> 2, h = t & 3;                   // gather: row of the tile, quarter of it
-        // softmax: TMEM lane quarter, quarter of the heads (16 heads: the first
-        // two take eight each)
-        const int q4 = warp & 3, c = warp >> 2;
-        const bool active = c * kCols < NH;
+        const int q4 = warp & 3, c = warp >> 2;            // TMEM lane quarter, half of the heads
         const int key = q4 * 32 + lane;
         const uint32_t lane_addr = (uint32_t)(q4 * 32) << 16;
-        bool ok = true;
-
-        // the query, as nc + 1 K-major blocks of 64 columns (absent heads and
-        // columns are zero-filled)
-        {
-            const int dqk = a.dc + a.dr;
-            const __nv_bfloat16 *q = a.q + (row * a.Hq + h0) * dqk;
-            for (int f = t; f < (nc + 1) * NH * 8; f += kWork) {
-                const int p = f & 7, head = (f >> 3) % NH, blk = (f >> 3) / NH;
-                const bool v = head < heads && blk * 64 + p * 8 < dqk;
-                cp_async16(qbase + blk * NH * 128 + head * 128 + ((p ^ (head & 7)) << 4),
-                           q + (v ? head * dqk + blk * 64 + p * 8 : 0), v ? 16u : 0u);
-            }
-            cp_async_arrive(&ctl.q_full);
-        }
-        int32_t trow = slot_row(a, list, lo + j < hi ? lo + j : a.slots, limit, done);
-        bool kv_ok = slot_row(a, list, lo + key < hi ? lo + key : a.slots, limit, done) >= 0;
-        RawRow<F> raw;
-        if constexpr (F != DSA_BF16) load_raw<F>(raw, a, rbase, trow, h);
-        // the share's last slot that counts bounds the walk
-        {
+        // the slot's rotary part (half c of it), one tile ahead
+        int32_t trow = slot_row(a, list, lo + key < hi ? lo + key : a.slots, limit, done);
+        uint4 rope[4];
+        load_rope<F>(rope, a, rbase, trow, c);
+        if (!count_all) {
             int last = -1;
-            for (int s = lo + t; s < hi; s += kWork)
+            for (int s = lo + t; s < hi; s += kSoft)
                 if (slot_row(a, list, s, limit, done) >= 0) last = s;
             last = __reduce_max_sync(0xffffffffu, last);
             if (lane == 0 && last >= 0) atomicMax(&ctl.last, last);
+            tc::named_barrier(2, kThreads);
+            tiles = ctl.last < lo ? 0 : (ctl.last - lo) / kTile + 1;
         }
-        tc::named_barrier(2, kThreads);
-        const int tiles = ctl.last < lo ? 0 : (ctl.last - lo) / kTile + 1;
         float lsum[kCols];
 #pragma unroll
         for (int e = 0; e < kCols; e++) lsum[e] = 0.f;
-
+        const uint32_t scol = tmem + lane_addr + c * kCols;
         for (int i = 0; i < tiles; i++) {
-            const uint32_t ph = i & 1, prev = ph ^ 1;
-            // ------------------------------------------------ the tile's rows
-            if constexpr (F == DSA_BF16) {
-                if (h == 0) ctl.list[j] = trow;
-                tc::named_barrier(1, kWork);
-                for (int m = 0; m <= mt; m++) {
-                    // chunk pair m is free once the last tile's value mix m is
-                    // complete; the rotary chunk (and P) once all of it is
-                    if (i > 0 && m < mt && !tc::mbar_wait(&ctl.o_done[m], prev, a.err, abort)) ok = false;
-                    for (int k = 2 * m; k < (m < mt ? 2 * m + 2 : 2 * m + 1); k++) {
+            // P gives the rotary chunk its place back once the value mix of
+            // the tile before is complete
+            if (i > 0 && !tc::mbar_wait(&ctl.o_done[mt - 1], (i - 1) & 1, a.err, abort)) ok = false;
 #pragma unroll
-                        for (int u = 0; u < kTile * 8 / kWork; u++) {
-                            const int f = t + u * kWork, r = f >> 3, p = f & 7;
-                            const int32_t tr = ctl.list[r];
-                            const bool v = tr >= 0 && k * 64 + p * 8 < a.dc + a.dr;
-                            cp_async16(tile + k * kRegion + r * 128 + ((p ^ (r & 7)) << 4),
-                                       a.kv + (rbase + (v ? tr : 0)) * a.row_bytes + (v ? k * 128 + p * 16 : 0),
-                                       v ? 16u : 0u);
-                        }
-                    }
-                    cp_async_arrive(&ctl.full[m < mt ? m : 4]);
-                }
-            } else {
-#pragma unroll
-                for (int m = 0; m < 4; m++) {
-                    if (m >= mt) break;
-                    if (i > 0 && !tc::mbar_wait(&ctl.o_done[m], prev, a.err, abort)) ok = false;
-                    store_pair<F>(raw, m, tile, h, j);
-                    tc::fence_proxy_async_smem();
-                    tc::mbar_arrive(&ctl.full[m]);
-                }
-#pragma unroll
-                for (int p = 0; p < 2; p++)
-                    st_shared_v4(pbase + j * 128 + (((2 * h + p) ^ (j & 7)) << 4), raw.rope[p]);
-                tc::fence_proxy_async_smem();
-                tc::mbar_arrive(&ctl.full[4]);
-            }
-            const bool valid = kv_ok;
+            for (int p = 0; p < 4; p++) st_shared_v4(pbase + key * 128 + (((4 * c + p) ^ (key & 7)) << 4), rope[p]);
+            tc::fence_proxy_async_smem();
+            tc::mbar_arrive(&ctl.full[4]);
+            const bool valid = trow >= 0;
             if (i + 1 < tiles) {
-                const int s0 = lo + (i + 1) * kTile;
-                trow = slot_row(a, list, s0 + j < hi ? s0 + j : a.slots, limit, done);
-                kv_ok = slot_row(a, list, s0 + key < hi ? s0 + key : a.slots, limit, done) >= 0;
-                if constexpr (F == DSA_BF16) {
-                    if (h == 0 && trow >= 0)
-                        tc::prefetch_l2_bulk(a.kv + (rbase + trow) * a.row_bytes, (uint32_t)a.row_bytes);
-                } else {
-                    load_raw<F>(raw, a, rbase, trow, h);
-                }
+                const int s1 = lo + (i + 1) * kTile + key;
+                trow = slot_row(a, list, s1 < hi ? s1 : a.slots, limit, done);
+                load_rope<F>(rope, a, rbase, trow, c);
             }
-            // ---------------------------------------------------- softmax
-            if (!tc::mbar_wait(&ctl.s_done, ph, a.err, abort)) ok = false;
+            if (!tc::mbar_wait(&ctl.s_done, i & 1, a.err, abort)) ok = false;
             tc::tc_fence_after();
-            float z[kCols];
             bool over = false;
-            if (active) {
-                uint32_t v[kCols];
-                ld_cols(tmem + lane_addr + c * kCols, v);
+#pragma unroll
+            for (int x = 0; x < kCols; x += kStep) {
+                uint32_t v[kStep];
+                ld_cols(scol + x, v);
                 tc::tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < kCols; e++) z[e] = __uint_as_float(v[e]) * a.scale_log2;
+                for (int e = 0; e < kStep; e += 4) {
+                    const float4 r = *reinterpret_cast<const float4 *>(&ctl.lim[c * kCols + x + e]);
+                    over |= __uint_as_float(v[e]) * a.scale_log2 > r.x || __uint_as_float(v[e + 1]) * a.scale_log2 > r.y ||
+                            __uint_as_float(v[e + 2]) * a.scale_log2 > r.z || __uint_as_float(v[e + 3]) * a.scale_log2 > r.w;
+                }
             }
-#pragma unroll
-            for (int e = 0; active && e < kCols; e += 4) {
-                const float4 r = *reinterpret_cast<const float4 *>(&ctl.ref[c * kCols + e]);
-                const float rs[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-                for (int x = 0; x < 4; x++) over |= z[e + x] > rs[x] + kSlack;
-            }
-            if (tc::named_barrier_any(1, kWork, over && valid)) {
+            if (tc::named_barrier_any(1, kSoft, over && valid)) {
                 // new references: the tile's maxima, per lane quarter and then
                 // over the four
 #pragma unroll
-                for (int e = 0; active && e < kCols; e++) {
-                    const float m = warp_max_redux(valid ? z[e] : -INFINITY);
-                    if (lane == e) ctl.red[q4][c * kCols + e] = m;
+                for (int x = 0; x < kCols; x += kStep) {
+                    uint32_t v[kStep];
+                    ld_cols(scol + x, v);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < kStep; e++) {
+                        const float m = warp_max_redux(valid ? __uint_as_float(v[e]) * a.scale_log2 : -INFINITY);
+                        if (lane == e) ctl.red[q4][c * kCols + x + e] = m;
+                    }
                 }
-                tc::named_barrier(1, kWork);
+                tc::named_barrier(1, kSoft);
                 if (t < NH) {
                     const float old = ctl.ref[t];
                     const float m = fmaxf(fmaxf(fmaxf(ctl.red[0][t], ctl.red[1][t]),
                                                 fmaxf(ctl.red[2][t], ctl.red[3][t])), old);
                     ctl.fac[t] = old == m ? 1.f : ex2(old - m);
                     ctl.ref[t] = m;
+                    ctl.lim[t] = m + kSlack;
                     ctl.sub[t] = m == -INFINITY ? 0.f : m;
                 }
-                tc::named_barrier(1, kWork);
-                if (i > 0 && active) {
+                tc::named_barrier(1, kSoft);
+                if (i > 0) {
+                    // (the value mix of the tile before is complete: this
+                    // tile's logits were issued after it)
 #pragma unroll
                     for (int e = 0; e < kCols; e++) lsum[e] *= ctl.fac[c * kCols + e];
+#pragma unroll 1
                     for (int m = 0; m < mt; m++) {
-#pragma unroll
-                        for (int u = 0; u < kCols / 8; u++) {
-                            const uint32_t col = tmem + lane_addr + NH * (m + 1) + c * kCols + 8 * u;
+#pragma unroll 1
+                        for (int x = 0; x < kCols; x += 8) {
+                            const uint32_t col = scol + NH * (m + 1) + x;
                             uint32_t v[8];
                             tc::tmem_ld8(col, v);
                             tc::tmem_wait_ld();
 #pragma unroll
                             for (int e = 0; e < 8; e++)
-                                v[e] = __float_as_uint(__uint_as_float(v[e]) * ctl.fac[c * kCols + 8 * u + e]);
+                                v[e] = __float_as_uint(__uint_as_float(v[e]) * ctl.fac[c * kCols + x + e]);
                             tc::tmem_st8(col, v);
                         }
                     }
@@ -428,121 +407,201 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
                 }
             }
 #pragma unroll
-            for (int u = 0; active && u < kCols / 8; u++) {
-                const float4 s0 = *reinterpret_cast<const float4 *>(&ctl.sub[c * kCols + 8 * u]);
-                const float4 s1 = *reinterpret_cast<const float4 *>(&ctl.sub[c * kCols + 8 * u + 4]);
-                const float sub[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-                uint32_t pk[4];
+            for (int x = 0; x < kCols; x += kStep) {
+                uint32_t v[kStep];
+                ld_cols(scol + x, v);
+                tc::tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const int x = 8 * u + 2 * e;
-                    const float p0 = valid ? ex2(z[x] - sub[2 * e]) : 0.f;
-                    const float p1 = valid ? ex2(z[x + 1] - sub[2 * e + 1]) : 0.f;
-                    lsum[x] += p0;
-                    lsum[x + 1] += p1;
-                    pk[e] = bf16x2_bits(__floats2bfloat162_rn(p0, p1));
+                for (int u = 0; u < kStep / 8; u++) {
+                    const float4 s0 = *reinterpret_cast<const float4 *>(&ctl.sub[c * kCols + x + 8 * u]);
+                    const float4 s1 = *reinterpret_cast<const float4 *>(&ctl.sub[c * kCols + x + 8 * u + 4]);
+                    const float sub[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+                    uint32_t pk[4];
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        const float p0 = valid ? ex2(fmaf(__uint_as_float(v[8 * u + e]), a.scale_log2, -sub[e])) : 0.f;
+                        const float p1 = valid ? ex2(fmaf(__uint_as_float(v[8 * u + e + 1]), a.scale_log2, -sub[e + 1])) : 0.f;
+                        lsum[x + 8 * u + e] += p0;
+                        lsum[x + 8 * u + e + 1] += p1;
+                        pk[e / 2] = bf16x2_bits(__floats2bfloat162_rn(p0, p1));
+                    }
+                    st_shared_v4(pbase + key * 128 + (((c * (kCols / 8) + x / 8 + u) ^ (key & 7)) << 4),
+                                 make_uint4(pk[0], pk[1], pk[2], pk[3]));
                 }
-                st_shared_v4(pbase + key * 128 + (((c * (kCols / 8) + u) ^ (key & 7)) << 4),
-                             make_uint4(pk[0], pk[1], pk[2], pk[3]));
             }
             tc::fence_proxy_async_smem();
             tc::tc_fence_before();
             tc::mbar_arrive(&ctl.p_full);
         }
-        // -------------------------------------------------------- epilogue
-        if (tiles > 0 && active) {
+        // the heads' sums, over the warp's slots and then over the lane quarters
 #pragma unroll
-            for (int e = 0; e < kCols; e++) {
-                const float s = warp_sum(lsum[e]);
-                if (lane == e) ctl.red[q4][c * kCols + e] = s;
-            }
+        for (int e = 0; e < kCols; e++) {
+            const float s = warp_sum(lsum[e]);
+            if (lane == e) ctl.red[q4][c * kCols + e] = s;
         }
-        tc::named_barrier(1, kWork);
-        const int64_t unit = blockIdx.x;
+        tc::named_barrier(1, kSoft);
         if (t < heads) {
-            const float l = tiles ? (ctl.red[0][t] + ctl.red[1][t]) + (ctl.red[2][t] + ctl.red[3][t]) : 0.f;
+            const float l = (ctl.red[0][t] + ctl.red[1][t]) + (ctl.red[2][t] + ctl.red[3][t]);
             // (l is NaN where a logit is: it passes through)
             ctl.fac[t] = l == 0.f ? 0.f : 1.f / l;
             if (a.splits > 1)
-                a.part_ml[unit * NH + t] = make_float2(l == 0.f ? -INFINITY : ctl.ref[t], l);
+                a.part_ml[(int64_t)blockIdx.x * NH + t] = make_float2(l == 0.f ? -INFINITY : ctl.ref[t], l);
             else if (a.lse)
                 a.lse[row * a.Hq + h0 + t] = l == 0.f ? -INFINITY : (ctl.ref[t] + log2f(l)) * kLn2;
         }
-        tc::named_barrier(1, kWork);
-        if (tiles == 0) {
-            // nothing selected: zeros (a split's empty partial is its -inf alone)
-            if (a.splits == 1)
-                for (int f = t; f < heads * a.dc / 8; f += kWork)
-                    reinterpret_cast<uint4 *>(a.out + (row * a.Hq + h0) * a.dc)[f] = make_uint4(0, 0, 0, 0);
-            tc::mbar_wait(&ctl.q_full, 0, a.err, abort);
-        } else {
-            const uint32_t ph = (tiles - 1) & 1;
-            for (int m = 0; m < mt; m++) {
-                if (!tc::mbar_wait(&ctl.o_done[m], ph, a.err, abort)) ok = false;
-                tc::tc_fence_after();
-                // thread = (column of dc, quarter of the heads): a warp stores 32
-                // consecutive columns of one head at a time
-                const int col = m * 128 + key;
-                if (active) {
-                    uint32_t v[kCols];
-                    ld_cols(tmem + lane_addr + NH * (m + 1) + c * kCols, v);
-                    tc::tmem_wait_ld();
+    } else if (warp < kWork / 32) {
+        const int t = threadIdx.x - kSoft, pwarp = t >> 5;
+        const int j = t >> 1, h = t & 1;                   // row of the tile, half of it
+        const int dqk = a.dc + a.dr;
+        int32_t trow = slot_row(a, list, lo + j < hi ? lo + j : a.slots, limit, done);
+        RawRow<F> raw;
+        if constexpr (F != DSA_BF16) load_raw<F>(raw, a, rbase, trow, h);
+        // the query, as nc + 1 K-major blocks of 64 columns (absent heads and
+        // columns are zero-filled)
+        const __nv_bfloat16 *q = a.q + (row * a.Hq + h0) * dqk;
+        for (int f = t; f < (nc + 1) * NH * 8; f += kProd) {
+            const int p = f & 7, head = (f >> 3) % NH, blk = (f >> 3) / NH;
+            const bool v = head < heads && blk * 64 + p * 8 < dqk;
+            cp_async16(qbase + blk * NH * 128 + head * 128 + ((p ^ (head & 7)) << 4),
+                       q + (v ? head * dqk + blk * 64 + p * 8 : 0), v ? 16u : 0u);
+        }
+        cp_async_arrive(&ctl.q_full);
+        if (!count_all) {
+            tc::named_barrier(2, kThreads);
+            tiles = ctl.last < lo ? 0 : (ctl.last - lo) / kTile + 1;
+        }
+        for (int i = 0; i < tiles; i++) {
+            // chunk pair m is free once the value mix m of the tile before is
+            // complete; the rotary chunk (and P) once all of it is
 #pragma unroll
-                    for (int e = 0; e < kCols; e++) {
-                        const int hd = c * kCols + e;
-                        if (hd >= heads || !ok) continue;
-                        if (a.splits > 1)
-                            a.part_o[(unit * NH + hd) * a.dc + col] = __uint_as_float(v[e]);
-                        else
-                            a.out[(row * a.Hq + h0 + hd) * a.dc + col] =
-                                __float2bfloat16_rn(__uint_as_float(v[e]) * ctl.fac[hd]);
-                    }
+            for (int m = 0; m < 4; m++) {
+                if (m >= mt) break;
+                if (i > 0 && !tc::mbar_wait(&ctl.o_done[m], (i - 1) & 1, a.err, abort)) ok = false;
+                if constexpr (F == DSA_BF16) {
+                    copy_chunk(a, rbase, trow, 256 * m, tile + 2 * m * kRegion, pwarp, lane);
+                    copy_chunk(a, rbase, trow, 256 * m + 128, tile + (2 * m + 1) * kRegion, pwarp, lane);
+                    cp_async_arrive(&ctl.full[m]);
+                } else {
+                    store_pair<F>(raw, m, tile, h, j);
+                    tc::fence_proxy_async_smem();
+                    tc::mbar_arrive(&ctl.full[m]);
+                }
+            }
+            if (i + 1 < tiles) {
+                const int s1 = lo + (i + 1) * kTile + j;
+                trow = slot_row(a, list, s1 < hi ? s1 : a.slots, limit, done);
+                if constexpr (F == DSA_BF16) {
+                    if (h == 0 && trow >= 0)
+                        tc::prefetch_l2_bulk(a.kv + (rbase + trow) * a.row_bytes, (uint32_t)a.row_bytes);
+                } else {
+                    load_raw<F>(raw, a, rbase, trow, h);
                 }
             }
         }
+        if (!tc::mbar_wait(&ctl.q_full, 0, a.err, abort)) ok = false;
     } else {
         // ------------------------------------------------------------- MMA
-        tc::named_barrier(2, kThreads);
-        const int tiles = ctl.last < lo ? 0 : (ctl.last - lo) / kTile + 1;
-        if (lane == 0) {
+        if (!count_all) {
+            tc::named_barrier(2, kThreads);
+            tiles = ctl.last < lo ? 0 : (ctl.last - lo) / kTile + 1;
+        }
+        {
+            // (the whole warp walks, one elected lane issues: uniform control
+            // keeps the descriptors in uniform registers)
             const uint32_t id_qk = tc::instr_desc(tc::kFmtBF16, tc::kFmtBF16, 128, NH);
             const uint32_t id_pv = tc::instr_desc(tc::kFmtBF16, tc::kFmtBF16, 128, NH, true, true);
-            bool ok = tiles > 0 && tc::mbar_wait(&ctl.q_full, 0, a.err, abort);
+            // (descriptors count 16-byte units: one add per MMA, so that the
+            // issue keeps ahead of the tensor core)
+            const uint64_t kd0 = tc::smem_desc(tile, 1024, tc::kSwizzle128B);
+            const uint64_t qd0 = tc::smem_desc(qbase, 1024, tc::kSwizzle128B);
+            const uint64_t vd0 = tc::smem_desc(tile, 1024, tc::kSwizzle128B, kRegion);
+            const uint64_t pd0 = tc::smem_desc(pbase, 1024, tc::kSwizzle128B, kRegion);
+            const int rope_steps = (a.dr + 15) / 16;
+            ok = tiles > 0 && tc::mbar_wait(&ctl.q_full, 0, a.err, abort);
+            tc::fence_proxy_async_smem();                  // the query came by cp.async
             for (int i = 0; ok && i < tiles; i++) {
                 const uint32_t ph = i & 1;
-                for (int m = 0; ok && m <= mt; m++) {
-                    ok = tc::mbar_wait(&ctl.full[m < mt ? m : 4], ph, a.err, abort);
-                    // written through the generic proxy (cp.async or stores)
-                    tc::fence_proxy_async_smem();
+                // (the threads that store fence before they arrive; behind
+                // cp.async the fence is this thread's)
+                for (int m = 0; ok && m < mt; m++) {
+                    ok = tc::mbar_wait(&ctl.full[m], ph, a.err, abort);
+                    if (F == DSA_BF16) tc::fence_proxy_async_smem();
                     tc::tc_fence_after();
-                    for (int k = 2 * m; ok && k < (m < mt ? 2 * m + 2 : 2 * m + 1); k++) {
-                        const int steps = k < nc ? 4 : (a.dr + 15) / 16;
-                        for (int ks = 0; ks < steps; ks++)
-                            tc::mma_f16(tmem, tc::smem_desc(tile + k * kRegion + ks * 32, 1024, tc::kSwizzle128B),
-                                        tc::smem_desc(qbase + k * NH * 128 + ks * 32, 1024, tc::kSwizzle128B),
-                                        id_qk, k > 0 || ks > 0);
+                    const uint64_t kd = kd0 + m * (2 * kRegion / 16), qd = qd0 + m * (2 * NH * 128 / 16);
+                    if (tc::elect_one()) {
+#pragma unroll
+                        for (int x = 0; x < 8; x++)
+                            tc::mma_f16(tmem, kd + (x >> 2) * (kRegion / 16) + (x & 3) * 2,
+                                        qd + (x >> 2) * (NH * 128 / 16) + (x & 3) * 2, id_qk, m > 0 || x > 0);
                     }
+                    __syncwarp();
                 }
-                if (!ok) break;
-                tc::tc_commit(&ctl.s_done);
+                if (!ok || !(ok = tc::mbar_wait(&ctl.full[4], ph, a.err, abort))) break;
+                tc::tc_fence_after();
+                if (tc::elect_one()) {
+                    for (int x = 0; x < rope_steps; x++)
+                        tc::mma_f16(tmem, kd0 + nc * (kRegion / 16) + x * 2, qd0 + nc * (NH * 128 / 16) + x * 2, id_qk,
+                                    true);
+                    tc::tc_commit(&ctl.s_done);
+                }
+                __syncwarp();
                 if (!(ok = tc::mbar_wait(&ctl.p_full, ph, a.err, abort))) break;
                 tc::tc_fence_after();
-                // step ks: slots [16 ks, 16 ks + 16) of the chunk pair (A, two
+                // step x: slots [16 x, 16 x + 16) of the chunk pair (A, two
                 // 64-column atoms 16 KB apart) and of P (B), both MN-major
-                for (int m = 0; m < mt; m++) {
-                    for (int ks = 0; ks < kTile / 16; ks++)
-                        tc::mma_f16(tmem + NH * (m + 1),
-                                    tc::smem_desc(tile + 2 * m * kRegion + ks * 2048, 1024, tc::kSwizzle128B, kRegion),
-                                    tc::smem_desc(pbase + ks * 2048, 1024, tc::kSwizzle128B, kRegion), id_pv,
-                                    i > 0 || ks > 0);
-                    tc::tc_commit(&ctl.o_done[m]);
+                if (tc::elect_one()) {
+                    for (int m = 0; m < mt; m++) {
+                        const uint64_t vd = vd0 + m * (2 * kRegion / 16);
+#pragma unroll
+                        for (int x = 0; x < kTile / 16; x++)
+                            tc::mma_f16(tmem + NH * (m + 1), vd + x * (2048 / 16), pd0 + x * (2048 / 16), id_pv,
+                                        i > 0 || x > 0);
+                        tc::tc_commit(&ctl.o_done[m]);
+                    }
                 }
+                __syncwarp();
             }
             // every issued MMA completes before TMEM is released
-            tc::tc_commit(&ctl.mma_fin);
+            if (tc::elect_one()) tc::tc_commit(&ctl.mma_fin);
+            __syncwarp();
             tc::mbar_wait(&ctl.mma_fin, 0, a.err, abort);
         }
         __syncwarp();
+    }
+    // ------------------------------------------------------------ epilogue
+    if (warp < kWork / 32) {
+        tc::named_barrier(3, kWork);
+        // thread = (column of dc, quarter of the heads; of 16 heads, the first
+        // two quarters take eight each): a warp stores 32 consecutive columns
+        // of one head at a time
+        const int q4 = warp & 3, c = warp >> 2;
+        if (tiles == 0) {
+            // nothing selected: zeros (a split's empty partial is its sum of 0)
+            if (a.splits == 1)
+                for (int f = threadIdx.x; f < heads * a.dc / 8; f += kWork)
+                    reinterpret_cast<uint4 *>(a.out + (row * a.Hq + h0) * a.dc)[f] = make_uint4(0, 0, 0, 0);
+        } else if (c * kOut < NH) {
+            for (int m = 0; m < mt; m++) {
+                if (!tc::mbar_wait(&ctl.o_done[m], (tiles - 1) & 1, a.err, abort)) ok = false;
+                tc::tc_fence_after();
+                uint32_t v[kOut];
+                ld_cols(tmem + ((uint32_t)(q4 * 32) << 16) + NH * (m + 1) + c * kOut, v);
+                tc::tmem_wait_ld();
+                const int col = m * 128 + q4 * 32 + lane;
+                const int n = ok ? heads - c * kOut : 0;   // heads of this thread
+                if (a.splits > 1) {
+                    float *o = a.part_o + ((int64_t)blockIdx.x * NH + c * kOut) * a.dc + col;
+#pragma unroll
+                    for (int e = 0; e < kOut; e++)
+                        if (e < n) o[e * a.dc] = __uint_as_float(v[e]);
+                } else {
+                    __nv_bfloat16 *o = a.out + (row * a.Hq + h0 + c * kOut) * a.dc + col;
+#pragma unroll
+                    for (int e = 0; e < kOut; e++)
+                        if (e < n) o[e * a.dc] = __float2bfloat16_rn(__uint_as_float(v[e]) * ctl.fac[c * kOut + e]);
+                }
+            }
+        }
     }
     tc::tc_fence_before();
     __syncthreads();
