@@ -20,22 +20,23 @@
 // output columns fill TMEM and each tile's result has to leave it.)
 //
 // One CTA = (query row, group of up to 64 heads, share of the row's slots).
-// Three roles, so that none holds another's registers:
-//   - eight producer warps decode the tile's rows to bf16 in 64-column chunks,
+// Sixteen work warps and one that issues the MMAs.  Per tile, a work warp
+//   - decodes the tile's rows (four threads a row) to bf16 in 64-column chunks,
 //     128B-swizzled K-major tiles that serve as the logits' A operand and, read
-//     MN-major, as the value mix's.  Quantised rows are loaded into registers
-//     one tile ahead (two threads a row) and decoded as the value mix of the
-//     tile before frees each pair of chunks; bf16 rows are copied by cp.async,
-//     their lines requested into L2 one tile ahead;
-//   - eight softmax warps: thread = (slot, half of the heads); the running
-//     maximum of each head is a reference kept until a logit passes it by more
-//     than 8 (2^8 in the weights, which bf16 and the fp32 sums hold at full
-//     precision); only then are the tile's maxima reduced and the output
-//     rescaled.  Sums stay per thread in fp32 and are reduced once at the end;
-//     the weights are rounded to bf16 as MMA operands (the sums take them
-//     unrounded).  They also hold the next tile's rotary parts, which go where
-//     the weights were once the value mix has read those;
-//   - one thread issues the MMAs.
+//     MN-major, as the value mix's, as the value mix of the tile before frees
+//     each pair of chunks.  Quantised rows wait in registers since one tile
+//     ahead; bf16 rows are copied by cp.async, their lines requested into L2
+//     one tile ahead.  The weights P take the place of the rotary chunk, which
+//     the logits have read by then;
+//   - loads the next tile's rows;
+//   - takes the softmax of (slot, quarter of the heads): the running maximum of
+//     each head is a reference kept until a logit passes it by more than 8 (2^8
+//     in the weights, which bf16 and the fp32 sums hold at full precision);
+//     only then are the tile's maxima reduced and the output rescaled.  Sums
+//     stay per thread in fp32 and are reduced once at the end; the weights are
+//     rounded to bf16 as MMA operands (the sums take them unrounded).
+// Shared memory bounds the walk: a 128 x 64 x 16 MMA reads 6 KB in its 49
+// cycles, and the decoded tile is written beside it.
 // Splits of a row (when there are fewer rows than SMs) leave fp32 partials that
 // a second kernel merges.
 #include "latent_rows.cuh"
@@ -46,8 +47,7 @@ namespace {
 
 constexpr int kTile = 128;                      // slots per tile (the MMA M of the logits)
 constexpr int kRegion = kTile * 128;            // one 64-column chunk of a tile: 16 KB
-constexpr int kSoft = 256, kProd = 256;         // softmax threads, producer threads
-constexpr int kWork = kSoft + kProd;
+constexpr int kWork = 512;                      // work threads
 constexpr int kThreads = kWork + 32;
 constexpr int kMaxHeads = 64;                   // heads per CTA
 constexpr float kLog2e = 1.4426950408889634f;
@@ -83,6 +83,7 @@ struct alignas(16) Control {
     uint32_t tmem;
     int abort;
     int last;                   // last slot of the share that counts
+    uint8_t valid[2][kTile / 8];   // per tile parity: one bit per slot that counts
 };
 
 size_t smem_bytes(int dc, int nh) {
@@ -104,6 +105,11 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
 __device__ __forceinline__ uint4 ld_v4(const void *p) {
     uint4 v;
     asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint2 ld_v2(const void *p) {
+    uint2 v;
+    asm volatile("ld.global.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
     return v;
 }
 __device__ __forceinline__ uint32_t ld_b32(const void *p) {
@@ -149,91 +155,95 @@ __device__ __forceinline__ int32_t slot_row(const AttnArgs &a, const int32_t *li
     return t < 0 || t > limit ? -1 : t;
 }
 
-// What a producer holds of its row of the next tile: chunks 2m + h, h = the
-// thread's half of the row's chunk pairs.
+// What a thread holds of its row of the next tile: of each chunk pair m the
+// half h & 1 of chunk 2m + (h >> 1), h = the thread's quarter of the row, and a
+// quarter of the rotary part.
 template <int F> struct RawRow;
 template <> struct RawRow<DSA_Q4_LATENT> {
-    uint4 code[4][2];
-    uint32_t scale[4];          // of both pieces
+    uint4 code[4];
+    uint2 scale;                // groups 4 h .. 4 h + 3 (pair h's)
+    uint4 rope[2];
 };
 template <> struct RawRow<DSA_FP8_LATENT> {
-    uint4 code[4][4];
+    uint4 code[4][2];
     float scale[4];
+    uint4 rope[2];
 };
-template <> struct RawRow<DSA_BF16> {};
+template <> struct RawRow<DSA_BF16> {
+    uint4 rope[2];
+};
 
 template <int F>
 __device__ __forceinline__ void load_raw(RawRow<F> &r, const AttnArgs &a, int64_t rbase, int32_t t, int h) {
     const uint8_t *row = a.kv + (rbase + (t < 0 ? 0 : t)) * a.row_bytes;
     const bool v = t >= 0;
-    const bool wide = F == DSA_Q4_LATENT || (a.row_bytes & 15) == 0;
+    // (FP8 rows of other widths than 512 are only 4-byte aligned)
+    const bool wide = F != DSA_FP8_LATENT || (a.row_bytes & 15) == 0;
     const uint4 zero = make_uint4(0, 0, 0, 0);
     const int mt = a.dc / 128;
-#pragma unroll
-    for (int m = 0; m < 4; m++) {
-        const bool on = v && m < mt;
-        if constexpr (F == DSA_Q4_LATENT) {
-            // (the half-1 thread takes its two pieces in the other order: with
-            // the swizzle, the four rows x two threads that store together then
-            // touch all banks once)
-            r.code[m][0] = on ? ld_v4(row + 64 * m + 32 * h + 16 * h) : zero;
-            r.code[m][1] = on ? ld_v4(row + 64 * m + 32 * h + 16 * (h ^ 1)) : zero;
-            r.scale[m] = on ? ld_b32(row + latent_q4_scales_at(a.dc, a.dr) + 8 * m + 4 * h) : 0u;
-        } else {
-#pragma unroll
-            for (int p = 0; p < 4; p++)
-                r.code[m][p] = on ? ld_piece(row + 128 * m + 64 * h + 16 * (p ^ (2 * h)), wide) : zero;
-            r.scale[m] = on ? __uint_as_float(ld_b32(row + a.dc + 4 * m)) : 0.f;
-        }
-    }
-}
-
-// Decodes the thread's half of chunk pair m into the tile.
-template <int F>
-__device__ __forceinline__ void store_pair(const RawRow<F> &r, int m, uint32_t tile, int h, int j) {
-    const uint32_t dst = tile + (2 * m + h) * kRegion + j * 128;
-    const int sw = j & 7;
     if constexpr (F == DSA_Q4_LATENT) {
 #pragma unroll
-        for (int p = 0; p < 2; p++) {
-            const int piece = p ^ h;
-            const __nv_bfloat16 s1 = __ushort_as_bfloat16((uint16_t)(r.scale[m] >> (16 * piece)));
-            const __nv_bfloat162 s = __halves2bfloat162(s1, s1);
-            const uint32_t w[4] = {r.code[m][p].x, r.code[m][p].y, r.code[m][p].z, r.code[m][p].w};
+        for (int m = 0; m < 4; m++) r.code[m] = v && m < mt ? ld_v4(row + 64 * m + 16 * h) : zero;
+        r.scale = v && h < mt ? ld_v2(row + latent_q4_scales_at(a.dc, a.dr) + 8 * h) : make_uint2(0, 0);
+    } else if constexpr (F == DSA_FP8_LATENT) {
 #pragma unroll
-            for (int u = 0; u < 4; u++) st_shared_v4(dst + (((4 * piece + u) ^ sw) << 4), q4_decode8(w[u], s));
+        for (int m = 0; m < 4; m++) {
+#pragma unroll
+            for (int p = 0; p < 2; p++)
+                r.code[m][p] = v && m < mt ? ld_piece(row + 128 * m + 32 * h + 16 * (p ^ (h >> 1)), wide) : zero;
+            r.scale[m] = v && m < mt ? __uint_as_float(ld_b32(row + a.dc + 4 * m)) : 0.f;
         }
     } else {
+        if (v && h == 0) tc::prefetch_l2_bulk(row, (uint32_t)a.row_bytes);
+    }
+    const uint8_t *pe = row + latent_rope_at<F>(a.dc);
 #pragma unroll
-        for (int p = 0; p < 4; p++) {
-            const int piece = p ^ (2 * h);
+    for (int p = 0; p < 2; p++) {
+        const int piece = 2 * h + p;                       // values [8 piece, 8 piece + 8)
+        r.rope[p] = v && 8 * piece < a.dr ? ld_piece(pe + 16 * piece, wide) : zero;
+    }
+}
+
+// Decodes the thread's share of chunk pair m into the tile.  The threads of
+// the upper chunk (h >> 1 = 1) store their four 16-byte units in the order 2,
+// 3, 0, 1: with the swizzle, the two rows x four threads that store together
+// then touch all banks once.
+template <int F>
+__device__ __forceinline__ void store_pair(const RawRow<F> &r, int m, uint32_t tile, int h, int j) {
+    const uint32_t dst = tile + (2 * m + (h >> 1)) * kRegion + j * 128;
+    const int sw = j & 7, up = h >> 1, u0 = 4 * (h & 1);
+    if constexpr (F == DSA_Q4_LATENT) {
+        // group 4 m + h: element h of what the row's thread m holds
+        const uint32_t x = __shfl_sync(0xffffffffu, r.scale.x, m, 4), y = __shfl_sync(0xffffffffu, r.scale.y, m, 4);
+        const uint32_t two = up ? y : x;
+        const __nv_bfloat16 s1 = __ushort_as_bfloat16((uint16_t)((h & 1) ? two >> 16 : two));
+        const __nv_bfloat162 s = __halves2bfloat162(s1, s1);
+        const uint4 c = r.code[m];
+        const uint32_t w[4] = {up ? c.z : c.x, up ? c.w : c.y, up ? c.x : c.z, up ? c.y : c.w};
+#pragma unroll
+        for (int u = 0; u < 4; u++)
+            st_shared_v4(dst + (((u0 + (u ^ (2 * up))) ^ sw) << 4), q4_decode8(w[u], s));
+    } else if constexpr (F == DSA_FP8_LATENT) {
+#pragma unroll
+        for (int p = 0; p < 2; p++) {
+            const int u = u0 + 2 * (p ^ up);
             const uint4 w = r.code[m][p];
-            st_shared_v4(dst + (((2 * piece) ^ sw) << 4), fp8_decode8(w.x, w.y, r.scale[m]));
-            st_shared_v4(dst + (((2 * piece + 1) ^ sw) << 4), fp8_decode8(w.z, w.w, r.scale[m]));
+            st_shared_v4(dst + ((u ^ sw) << 4), fp8_decode8(w.x, w.y, r.scale[m]));
+            st_shared_v4(dst + (((u + 1) ^ sw) << 4), fp8_decode8(w.z, w.w, r.scale[m]));
         }
     }
 }
 
-// Values [32 c, 32 c + 32) of a row's rotary part (zeros past its width).
-template <int F>
-__device__ __forceinline__ void load_rope(uint4 (&r)[4], const AttnArgs &a, int64_t rbase, int32_t t, int c) {
-    const uint8_t *pe = a.kv + (rbase + (t < 0 ? 0 : t)) * a.row_bytes + latent_rope_at<F>(a.dc) + 64 * c;
-    const bool wide = F != DSA_FP8_LATENT || (a.row_bytes & 15) == 0;
-#pragma unroll
-    for (int p = 0; p < 4; p++)
-        r[p] = t >= 0 && 32 * c + 8 * p < a.dr ? ld_piece(pe + 16 * p, wide) : make_uint4(0, 0, 0, 0);
-}
-
-// Copies 128 bytes of each of the warp's sixteen bf16 rows, from byte `at`, into
+// Copies 128 bytes of each of the warp's eight bf16 rows, from byte `at`, into
 // a chunk (zeros for an empty slot).  Eight lanes copy a row; row r's cache row
-// is held by lane 2 r.
+// is held by lane 4 r.
 __device__ __forceinline__ void copy_chunk(const AttnArgs &a, int64_t rbase, int32_t trow, int at, uint32_t chunk,
-                                           int pwarp, int lane) {
+                                           int warp, int lane) {
     const int p = lane & 7;
 #pragma unroll
-    for (int u = 0; u < 4; u++) {
-        const int r = 4 * u + (lane >> 3), j = 16 * pwarp + r;
-        const int32_t t = __shfl_sync(0xffffffffu, trow, 2 * r);
+    for (int u = 0; u < 2; u++) {
+        const int r = 4 * u + (lane >> 3), j = 8 * warp + r;
+        const int32_t t = __shfl_sync(0xffffffffu, trow, 4 * r);
         cp_async16(chunk + j * 128 + ((p ^ (j & 7)) << 4), a.kv + (rbase + (t < 0 ? 0 : t)) * a.row_bytes + at + 16 * p,
                    t < 0 ? 0u : 16u);
     }
@@ -241,9 +251,9 @@ __device__ __forceinline__ void copy_chunk(const AttnArgs &a, int64_t rbase, int
 
 template <int F, int NH>
 __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs a) {
-    constexpr int kCols = NH / 2;                          // heads per softmax thread
+    // heads per work thread (of 16 heads, the first two quarters take eight each)
+    constexpr int kCols = NH == 16 ? 8 : NH / 4;
     constexpr int kStep = 8;                               // logits a softmax thread holds at a time
-    constexpr int kOut = NH == 16 ? 8 : NH / 4;            // heads per thread of the epilogue
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int nc = a.dc / 64, mt = a.dc / 128;             // latent chunks, dc tiles
@@ -259,11 +269,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
                            : NH * (mt + 1) <= 256 ? 256 : 512;
     if (warp == kWork / 32) {
         if (lane == 0) {
-            for (int i = 0; i < 4; i++) tc::mbar_init(&ctl.full[i], kProd);
-            tc::mbar_init(&ctl.full[4], kSoft);
-            tc::mbar_init(&ctl.q_full, kProd);
+            for (int i = 0; i < 5; i++) tc::mbar_init(&ctl.full[i], kWork);
+            tc::mbar_init(&ctl.q_full, kWork);
             tc::mbar_init(&ctl.s_done, 1);
-            tc::mbar_init(&ctl.p_full, kSoft);
+            tc::mbar_init(&ctl.p_full, kWork);
             tc::mbar_init(&ctl.mma_fin, 1);
             for (int i = 0; i < 4; i++) tc::mbar_init(&ctl.o_done[i], 1);
             ctl.abort = 0;
@@ -308,47 +317,83 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
     bool ok = true;
     int tiles = 1;
 
-    if (warp < kSoft / 32) {
+    if (warp < kWork / 32) {
         const int t = threadIdx.x;
-        const int q4 = warp & 3, c = warp >> 2;            // TMEM lane quarter, half of the heads
+        const int j = t >> 2, h = t & 3;                   // gather: row of the tile, quarter of it
+        const int q4 = warp & 3, c = warp >> 2;            // softmax: TMEM lane quarter, quarter of the heads
+        const bool active = c * kCols < NH;
         const int key = q4 * 32 + lane;
         const uint32_t lane_addr = (uint32_t)(q4 * 32) << 16;
-        // the slot's rotary part (half c of it), one tile ahead
-        int32_t trow = slot_row(a, list, lo + key < hi ? lo + key : a.slots, limit, done);
-        uint4 rope[4];
-        load_rope<F>(rope, a, rbase, trow, c);
+        const int dqk = a.dc + a.dr;
+        auto row_of = [&](int i) {                         // this thread's row of tile i
+            const int s = lo + i * kTile + j;
+            return slot_row(a, list, s < hi ? s : a.slots, limit, done);
+        };
+        int32_t trow = row_of(0);
+        RawRow<F> raw;
+        load_raw<F>(raw, a, rbase, trow, h);
+        // the query, as nc + 1 K-major blocks of 64 columns (absent heads and
+        // columns are zero-filled)
+        const __nv_bfloat16 *q = a.q + (row * a.Hq + h0) * dqk;
+        for (int f = t; f < (nc + 1) * NH * 8; f += kWork) {
+            const int p = f & 7, head = (f >> 3) % NH, blk = (f >> 3) / NH;
+            const bool v = head < heads && blk * 64 + p * 8 < dqk;
+            cp_async16(qbase + blk * NH * 128 + head * 128 + ((p ^ (head & 7)) << 4),
+                       q + (v ? head * dqk + blk * 64 + p * 8 : 0), v ? 16u : 0u);
+        }
+        cp_async_arrive(&ctl.q_full);
         if (!count_all) {
             int last = -1;
-            for (int s = lo + t; s < hi; s += kSoft)
+            for (int s = lo + t; s < hi; s += kWork)
                 if (slot_row(a, list, s, limit, done) >= 0) last = s;
             last = __reduce_max_sync(0xffffffffu, last);
             if (lane == 0 && last >= 0) atomicMax(&ctl.last, last);
             tc::named_barrier(2, kThreads);
             tiles = ctl.last < lo ? 0 : (ctl.last - lo) / kTile + 1;
         }
+        int32_t tnext = tiles > 1 ? row_of(1) : -1;
         float lsum[kCols];
 #pragma unroll
         for (int e = 0; e < kCols; e++) lsum[e] = 0.f;
         const uint32_t scol = tmem + lane_addr + c * kCols;
         for (int i = 0; i < tiles; i++) {
-            // P gives the rotary chunk its place back once the value mix of
-            // the tile before is complete
-            if (i > 0 && !tc::mbar_wait(&ctl.o_done[mt - 1], (i - 1) & 1, a.err, abort)) ok = false;
+            // chunk pair m is free once the value mix m of the tile before is
+            // complete; the rotary chunk (and P) once all of it is
 #pragma unroll
-            for (int p = 0; p < 4; p++) st_shared_v4(pbase + key * 128 + (((4 * c + p) ^ (key & 7)) << 4), rope[p]);
+            for (int m = 0; m < 4; m++) {
+                if (m >= mt) break;
+                if (i > 0 && !tc::mbar_wait(&ctl.o_done[m], (i - 1) & 1, a.err, abort)) ok = false;
+                if constexpr (F == DSA_BF16) {
+                    copy_chunk(a, rbase, trow, 256 * m, tile + 2 * m * kRegion, warp, lane);
+                    copy_chunk(a, rbase, trow, 256 * m + 128, tile + (2 * m + 1) * kRegion, warp, lane);
+                    cp_async_arrive(&ctl.full[m]);
+                } else {
+                    store_pair<F>(raw, m, tile, h, j);
+                    tc::fence_proxy_async_smem();
+                    tc::mbar_arrive(&ctl.full[m]);
+                }
+            }
+#pragma unroll
+            for (int p = 0; p < 2; p++) st_shared_v4(pbase + j * 128 + (((2 * h + p) ^ (j & 7)) << 4), raw.rope[p]);
+            {
+                // the warp's eight rows: one bit each
+                uint32_t x = __ballot_sync(0xffffffffu, trow >= 0) & 0x11111111u;
+                x = (x | x >> 3) & 0x03030303u;
+                x = (x | x >> 6) & 0x000F000Fu;
+                x = (x | x >> 12) & 0xFFu;
+                if (lane == 0) ctl.valid[i & 1][warp] = (uint8_t)x;
+            }
             tc::fence_proxy_async_smem();
             tc::mbar_arrive(&ctl.full[4]);
-            const bool valid = trow >= 0;
-            if (i + 1 < tiles) {
-                const int s1 = lo + (i + 1) * kTile + key;
-                trow = slot_row(a, list, s1 < hi ? s1 : a.slots, limit, done);
-                load_rope<F>(rope, a, rbase, trow, c);
-            }
+            trow = tnext;
+            if (i + 1 < tiles) load_raw<F>(raw, a, rbase, trow, h);
+            if (i + 2 < tiles) tnext = row_of(i + 2);
             if (!tc::mbar_wait(&ctl.s_done, i & 1, a.err, abort)) ok = false;
             tc::tc_fence_after();
+            const bool valid = ctl.valid[i & 1][key >> 3] >> (key & 7) & 1;
             bool over = false;
 #pragma unroll
-            for (int x = 0; x < kCols; x += kStep) {
+            for (int x = 0; active && x < kCols; x += kStep) {
                 uint32_t v[kStep];
                 ld_cols(scol + x, v);
                 tc::tmem_wait_ld();
@@ -359,11 +404,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
                             __uint_as_float(v[e + 2]) * a.scale_log2 > r.z || __uint_as_float(v[e + 3]) * a.scale_log2 > r.w;
                 }
             }
-            if (tc::named_barrier_any(1, kSoft, over && valid)) {
+            if (tc::named_barrier_any(1, kWork, over && valid)) {
                 // new references: the tile's maxima, per lane quarter and then
                 // over the four
 #pragma unroll
-                for (int x = 0; x < kCols; x += kStep) {
+                for (int x = 0; active && x < kCols; x += kStep) {
                     uint32_t v[kStep];
                     ld_cols(scol + x, v);
                     tc::tmem_wait_ld();
@@ -373,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
                         if (lane == e) ctl.red[q4][c * kCols + x + e] = m;
                     }
                 }
-                tc::named_barrier(1, kSoft);
+                tc::named_barrier(1, kWork);
                 if (t < NH) {
                     const float old = ctl.ref[t];
                     const float m = fmaxf(fmaxf(fmaxf(ctl.red[0][t], ctl.red[1][t]),
@@ -383,8 +428,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
                     ctl.lim[t] = m + kSlack;
                     ctl.sub[t] = m == -INFINITY ? 0.f : m;
                 }
-                tc::named_barrier(1, kSoft);
-                if (i > 0) {
+                tc::named_barrier(1, kWork);
+                if (i > 0 && active) {
                     // (the value mix of the tile before is complete: this
                     // tile's logits were issued after it)
 #pragma unroll
@@ -407,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
                 }
             }
 #pragma unroll
-            for (int x = 0; x < kCols; x += kStep) {
+            for (int x = 0; active && x < kCols; x += kStep) {
                 uint32_t v[kStep];
                 ld_cols(scol + x, v);
                 tc::tmem_wait_ld();
@@ -435,11 +480,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
         }
         // the heads' sums, over the warp's slots and then over the lane quarters
 #pragma unroll
-        for (int e = 0; e < kCols; e++) {
+        for (int e = 0; active && e < kCols; e++) {
             const float s = warp_sum(lsum[e]);
             if (lane == e) ctl.red[q4][c * kCols + e] = s;
         }
-        tc::named_barrier(1, kSoft);
+        tc::named_barrier(1, kWork);
         if (t < heads) {
             const float l = (ctl.red[0][t] + ctl.red[1][t]) + (ctl.red[2][t] + ctl.red[3][t]);
             // (l is NaN where a logit is: it passes through)
@@ -449,56 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
             else if (a.lse)
                 a.lse[row * a.Hq + h0 + t] = l == 0.f ? -INFINITY : (ctl.ref[t] + log2f(l)) * kLn2;
         }
-    } else if (warp < kWork / 32) {
-        const int t = threadIdx.x - kSoft, pwarp = t >> 5;
-        const int j = t >> 1, h = t & 1;                   // row of the tile, half of it
-        const int dqk = a.dc + a.dr;
-        int32_t trow = slot_row(a, list, lo + j < hi ? lo + j : a.slots, limit, done);
-        RawRow<F> raw;
-        if constexpr (F != DSA_BF16) load_raw<F>(raw, a, rbase, trow, h);
-        // the query, as nc + 1 K-major blocks of 64 columns (absent heads and
-        // columns are zero-filled)
-        const __nv_bfloat16 *q = a.q + (row * a.Hq + h0) * dqk;
-        for (int f = t; f < (nc + 1) * NH * 8; f += kProd) {
-            const int p = f & 7, head = (f >> 3) % NH, blk = (f >> 3) / NH;
-            const bool v = head < heads && blk * 64 + p * 8 < dqk;
-            cp_async16(qbase + blk * NH * 128 + head * 128 + ((p ^ (head & 7)) << 4),
-                       q + (v ? head * dqk + blk * 64 + p * 8 : 0), v ? 16u : 0u);
-        }
-        cp_async_arrive(&ctl.q_full);
-        if (!count_all) {
-            tc::named_barrier(2, kThreads);
-            tiles = ctl.last < lo ? 0 : (ctl.last - lo) / kTile + 1;
-        }
-        for (int i = 0; i < tiles; i++) {
-            // chunk pair m is free once the value mix m of the tile before is
-            // complete; the rotary chunk (and P) once all of it is
-#pragma unroll
-            for (int m = 0; m < 4; m++) {
-                if (m >= mt) break;
-                if (i > 0 && !tc::mbar_wait(&ctl.o_done[m], (i - 1) & 1, a.err, abort)) ok = false;
-                if constexpr (F == DSA_BF16) {
-                    copy_chunk(a, rbase, trow, 256 * m, tile + 2 * m * kRegion, pwarp, lane);
-                    copy_chunk(a, rbase, trow, 256 * m + 128, tile + (2 * m + 1) * kRegion, pwarp, lane);
-                    cp_async_arrive(&ctl.full[m]);
-                } else {
-                    store_pair<F>(raw, m, tile, h, j);
-                    tc::fence_proxy_async_smem();
-                    tc::mbar_arrive(&ctl.full[m]);
-                }
-            }
-            if (i + 1 < tiles) {
-                const int s1 = lo + (i + 1) * kTile + j;
-                trow = slot_row(a, list, s1 < hi ? s1 : a.slots, limit, done);
-                if constexpr (F == DSA_BF16) {
-                    if (h == 0 && trow >= 0)
-                        tc::prefetch_l2_bulk(a.kv + (rbase + trow) * a.row_bytes, (uint32_t)a.row_bytes);
-                } else {
-                    load_raw<F>(raw, a, rbase, trow, h);
-                }
-            }
-        }
-        if (!tc::mbar_wait(&ctl.q_full, 0, a.err, abort)) ok = false;
+        if (!tc::mbar_wait(&ctl.q_full, 0, a.err, abort)) ok = false;   // (own copies, when no tile was walked)
     } else {
         // ------------------------------------------------------------- MMA
         if (!count_all) {
@@ -571,34 +567,33 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
     // ------------------------------------------------------------ epilogue
     if (warp < kWork / 32) {
         tc::named_barrier(3, kWork);
-        // thread = (column of dc, quarter of the heads; of 16 heads, the first
-        // two quarters take eight each): a warp stores 32 consecutive columns
-        // of one head at a time
+        // thread = (column of dc, quarter of the heads): a warp stores 32
+        // consecutive columns of one head at a time
         const int q4 = warp & 3, c = warp >> 2;
         if (tiles == 0) {
             // nothing selected: zeros (a split's empty partial is its sum of 0)
             if (a.splits == 1)
                 for (int f = threadIdx.x; f < heads * a.dc / 8; f += kWork)
                     reinterpret_cast<uint4 *>(a.out + (row * a.Hq + h0) * a.dc)[f] = make_uint4(0, 0, 0, 0);
-        } else if (c * kOut < NH) {
+        } else if (c * kCols < NH) {
             for (int m = 0; m < mt; m++) {
                 if (!tc::mbar_wait(&ctl.o_done[m], (tiles - 1) & 1, a.err, abort)) ok = false;
                 tc::tc_fence_after();
-                uint32_t v[kOut];
-                ld_cols(tmem + ((uint32_t)(q4 * 32) << 16) + NH * (m + 1) + c * kOut, v);
+                uint32_t v[kCols];
+                ld_cols(tmem + ((uint32_t)(q4 * 32) << 16) + NH * (m + 1) + c * kCols, v);
                 tc::tmem_wait_ld();
                 const int col = m * 128 + q4 * 32 + lane;
-                const int n = ok ? heads - c * kOut : 0;   // heads of this thread
+                const int n = ok ? heads - c * kCols : 0;   // heads of this thread
                 if (a.splits > 1) {
-                    float *o = a.part_o + ((int64_t)blockIdx.x * NH + c * kOut) * a.dc + col;
+                    float *o = a.part_o + ((int64_t)blockIdx.x * NH + c * kCols) * a.dc + col;
 #pragma unroll
-                    for (int e = 0; e < kOut; e++)
+                    for (int e = 0; e < kCols; e++)
                         if (e < n) o[e * a.dc] = __uint_as_float(v[e]);
                 } else {
-                    __nv_bfloat16 *o = a.out + (row * a.Hq + h0 + c * kOut) * a.dc + col;
+                    __nv_bfloat16 *o = a.out + (row * a.Hq + h0 + c * kCols) * a.dc + col;
 #pragma unroll
-                    for (int e = 0; e < kOut; e++)
-                        if (e < n) o[e * a.dc] = __float2bfloat16_rn(__uint_as_float(v[e]) * ctl.fac[c * kOut + e]);
+                    for (int e = 0; e < kCols; e++)
+                        if (e < n) o[e * a.dc] = __float2bfloat16_rn(__uint_as_float(v[e]) * ctl.fac[c * kCols + e]);
                 }
             }
         }
