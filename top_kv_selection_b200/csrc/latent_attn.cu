@@ -21,10 +21,10 @@
 //
 // One CTA = (query row, group of up to 64 heads, share of the row's slots).
 // Sixteen work warps and one that issues the MMAs.  Per tile, a work warp
-//   - decodes the tile's rows (four threads a row) to bf16 in 64-column chunks,
-//     128B-swizzled K-major tiles that serve as the logits' A operand and, read
-//     MN-major, as the value mix's, as the value mix of the tile before frees
-//     each pair of chunks.  Quantised rows wait in registers since one tile
+//   - decodes the tile's rows (eight threads a row, two rows a thread) to bf16
+//     in 64-column chunks, 128B-swizzled K-major tiles that serve as the logits'
+//     A operand and, read MN-major, as the value mix's, as the value mix of the
+//     tile before frees each pair of chunks.  Quantised rows wait in registers since one tile
 //     ahead; bf16 rows are copied by cp.async, their lines requested into L2
 //     one tile ahead.  The weights P take the place of the rotary chunk, which
 //     the logits have read by then;
@@ -83,7 +83,7 @@ struct alignas(16) Control {
     uint32_t tmem;
     int abort;
     int last;                   // last slot of the share that counts
-    uint8_t valid[2][kTile / 8];   // per tile parity: one bit per slot that counts
+    uint8_t valid[2][kTile / 4];   // per tile parity: four slots a byte, a bit for each that counts
 };
 
 size_t smem_bytes(int dc, int nh) {
@@ -155,97 +155,88 @@ __device__ __forceinline__ int32_t slot_row(const AttnArgs &a, const int32_t *li
     return t < 0 || t > limit ? -1 : t;
 }
 
-// What a thread holds of its row of the next tile: of each chunk pair m the
-// half h & 1 of chunk 2m + (h >> 1), h = the thread's quarter of the row, and a
-// quarter of the rotary part.
-template <int F> struct RawRow;
-template <> struct RawRow<DSA_Q4_LATENT> {
-    uint4 code[4];
-    uint2 scale;                // groups 4 h .. 4 h + 3 (pair h's)
-    uint4 rope[2];
+// What a thread holds of the next tile: eight threads p share two rows.  Of
+// 4-bit codes a thread takes a group of its own row (row 0 for p < 4, else row
+// 1) in each chunk pair; of wider ones 16 bytes of every 128 of both rows.
+template <int F> struct RawRows;
+template <> struct RawRows<DSA_Q4_LATENT> {
+    uint4 code[4];              // groups 4 m + h, h = p & 3
+    uint2 scale;                // of groups 4 h .. 4 h + 3
+    uint4 rope0, rope1;
 };
-template <> struct RawRow<DSA_FP8_LATENT> {
-    uint4 code[4][2];
-    float scale[4];
-    uint4 rope[2];
+template <> struct RawRows<DSA_FP8_LATENT> {
+    uint4 x0[4], x1[4];         // codes [16 p, 16 p + 16) of block m
+    float s0, s1;               // block p & 3
+    uint4 rope0, rope1;
 };
-template <> struct RawRow<DSA_BF16> {
-    uint4 rope[2];
+template <> struct RawRows<DSA_BF16> {
+    uint4 rope0, rope1;
 };
 
 template <int F>
-__device__ __forceinline__ void load_raw(RawRow<F> &r, const AttnArgs &a, int64_t rbase, int32_t t, int h) {
-    const uint8_t *row = a.kv + (rbase + (t < 0 ? 0 : t)) * a.row_bytes;
-    const bool v = t >= 0;
+__device__ __forceinline__ void load_rows(RawRows<F> &r, const AttnArgs &a, int64_t rbase, int32_t t0, int32_t t1,
+                                          int p) {
+    const uint8_t *row0 = a.kv + (rbase + (t0 < 0 ? 0 : t0)) * a.row_bytes;
+    const uint8_t *row1 = a.kv + (rbase + (t1 < 0 ? 0 : t1)) * a.row_bytes;
+    const bool v0 = t0 >= 0, v1 = t1 >= 0;
     // (FP8 rows of other widths than 512 are only 4-byte aligned)
     const bool wide = F != DSA_FP8_LATENT || (a.row_bytes & 15) == 0;
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    const int mt = a.dc / 128;
     if constexpr (F == DSA_Q4_LATENT) {
+        const int h = p & 3;
+        const uint8_t *row = p < 4 ? row0 : row1;
+        const bool v = p < 4 ? v0 : v1;
 #pragma unroll
-        for (int m = 0; m < 4; m++) r.code[m] = v && m < mt ? ld_v4(row + 64 * m + 16 * h) : zero;
-        r.scale = v && h < mt ? ld_v2(row + latent_q4_scales_at(a.dc, a.dr) + 8 * h) : make_uint2(0, 0);
+        for (int m = 0; m < 4; m++) r.code[m] = v && 128 * m < a.dc ? ld_v4(row + 64 * m + 16 * h) : zero;
+        r.scale = v && 128 * h < a.dc ? ld_v2(row + latent_q4_scales_at(a.dc, a.dr) + 8 * h) : make_uint2(0, 0);
     } else if constexpr (F == DSA_FP8_LATENT) {
 #pragma unroll
         for (int m = 0; m < 4; m++) {
-#pragma unroll
-            for (int p = 0; p < 2; p++)
-                r.code[m][p] = v && m < mt ? ld_piece(row + 128 * m + 32 * h + 16 * (p ^ (h >> 1)), wide) : zero;
-            r.scale[m] = v && m < mt ? __uint_as_float(ld_b32(row + a.dc + 4 * m)) : 0.f;
+            r.x0[m] = v0 && 128 * m < a.dc ? ld_piece(row0 + 128 * m + 16 * p, wide) : zero;
+            r.x1[m] = v1 && 128 * m < a.dc ? ld_piece(row1 + 128 * m + 16 * p, wide) : zero;
         }
-    } else {
-        if (v && h == 0) tc::prefetch_l2_bulk(row, (uint32_t)a.row_bytes);
+        const bool on = 128 * (p & 3) < a.dc;
+        r.s0 = v0 && on ? __uint_as_float(ld_b32(row0 + a.dc + 4 * (p & 3))) : 0.f;
+        r.s1 = v1 && on ? __uint_as_float(ld_b32(row1 + a.dc + 4 * (p & 3))) : 0.f;
+    } else if (p == 0) {
+        if (v0) tc::prefetch_l2_bulk(row0, (uint32_t)a.row_bytes);
+        if (v1) tc::prefetch_l2_bulk(row1, (uint32_t)a.row_bytes);
     }
-    const uint8_t *pe = row + latent_rope_at<F>(a.dc);
-#pragma unroll
-    for (int p = 0; p < 2; p++) {
-        const int piece = 2 * h + p;                       // values [8 piece, 8 piece + 8)
-        r.rope[p] = v && 8 * piece < a.dr ? ld_piece(pe + 16 * piece, wide) : zero;
-    }
+    const int at = latent_rope_at<F>(a.dc) + 16 * p;
+    r.rope0 = v0 && 8 * p < a.dr ? ld_piece(row0 + at, wide) : zero;
+    r.rope1 = v1 && 8 * p < a.dr ? ld_piece(row1 + at, wide) : zero;
 }
 
-// Decodes the thread's share of chunk pair m into the tile.  The threads of
-// the upper chunk (h >> 1 = 1) store their four 16-byte units in the order 2,
-// 3, 0, 1: with the swizzle, the two rows x four threads that store together
-// then touch all banks once.
+// Decodes the thread's share of chunk pair m into the tile (rows j0, j1).  The
+// order in which a thread stores its 16-byte units is turned by its chunk, so
+// that with the swizzle eight threads that store together touch all banks once
+// (j1 differs from j0 in the lowest bit).
 template <int F>
-__device__ __forceinline__ void store_pair(const RawRow<F> &r, int m, uint32_t tile, int h, int j) {
-    const uint32_t dst = tile + (2 * m + (h >> 1)) * kRegion + j * 128;
-    const int sw = j & 7, up = h >> 1, u0 = 4 * (h & 1);
+__device__ __forceinline__ void store_pair(const RawRows<F> &r, int m, uint32_t tile, int p, int j0, int j1) {
     if constexpr (F == DSA_Q4_LATENT) {
-        // group 4 m + h: element h of what the row's thread m holds
+        // group 4 m + h: chunk 2 m + (h >> 1), units 4 (h & 1) + 0..3
+        const int h = p & 3, up = h >> 1, j = p < 4 ? j0 : j1, sw = j & 7;
         const uint32_t x = __shfl_sync(0xffffffffu, r.scale.x, m, 4), y = __shfl_sync(0xffffffffu, r.scale.y, m, 4);
         const uint32_t two = up ? y : x;
         const __nv_bfloat16 s1 = __ushort_as_bfloat16((uint16_t)((h & 1) ? two >> 16 : two));
         const __nv_bfloat162 s = __halves2bfloat162(s1, s1);
         const uint4 c = r.code[m];
         const uint32_t w[4] = {up ? c.z : c.x, up ? c.w : c.y, up ? c.x : c.z, up ? c.y : c.w};
+        const uint32_t dst = tile + (2 * m + up) * kRegion + j * 128;
 #pragma unroll
         for (int u = 0; u < 4; u++)
-            st_shared_v4(dst + (((u0 + (u ^ (2 * up))) ^ sw) << 4), q4_decode8(w[u], s));
+            st_shared_v4(dst + (((4 * (h & 1) + (u ^ (2 * up))) ^ sw) << 4), q4_decode8(w[u], s));
     } else if constexpr (F == DSA_FP8_LATENT) {
-#pragma unroll
-        for (int p = 0; p < 2; p++) {
-            const int u = u0 + 2 * (p ^ up);
-            const uint4 w = r.code[m][p];
-            st_shared_v4(dst + ((u ^ sw) << 4), fp8_decode8(w.x, w.y, r.scale[m]));
-            st_shared_v4(dst + (((u + 1) ^ sw) << 4), fp8_decode8(w.z, w.w, r.scale[m]));
-        }
-    }
-}
-
-// Copies 128 bytes of each of the warp's eight bf16 rows, from byte `at`, into
-// a chunk (zeros for an empty slot).  Eight lanes copy a row; row r's cache row
-// is held by lane 4 r.
-__device__ __forceinline__ void copy_chunk(const AttnArgs &a, int64_t rbase, int32_t trow, int at, uint32_t chunk,
-                                           int warp, int lane) {
-    const int p = lane & 7;
-#pragma unroll
-    for (int u = 0; u < 2; u++) {
-        const int r = 4 * u + (lane >> 3), j = 8 * warp + r;
-        const int32_t t = __shfl_sync(0xffffffffu, trow, 4 * r);
-        cp_async16(chunk + j * 128 + ((p ^ (j & 7)) << 4), a.kv + (rbase + (t < 0 ? 0 : t)) * a.row_bytes + at + 16 * p,
-                   t < 0 ? 0u : 16u);
+        // codes [16 p, 16 p + 16) of block m: chunk 2 m + (p >> 2), units 2 (p & 3) + 0, 1
+        const int up = p >> 2, u0 = 2 * (p & 3);
+        const float c0 = __shfl_sync(0xffffffffu, r.s0, m, 8), c1 = __shfl_sync(0xffffffffu, r.s1, m, 8);
+        const uint32_t dst = tile + (2 * m + up) * kRegion;
+        const uint4 a = r.x0[m], b = r.x1[m];
+        const int w0 = (u0 + up) ^ (j0 & 7), w1 = (u0 + up) ^ (j1 & 7);
+        st_shared_v4(dst + j0 * 128 + (w0 << 4), fp8_decode8(up ? a.z : a.x, up ? a.w : a.y, c0));
+        st_shared_v4(dst + j0 * 128 + ((w0 ^ 1) << 4), fp8_decode8(up ? a.x : a.z, up ? a.y : a.w, c0));
+        st_shared_v4(dst + j1 * 128 + (w1 << 4), fp8_decode8(up ? b.z : b.x, up ? b.w : b.y, c1));
+        st_shared_v4(dst + j1 * 128 + ((w1 ^ 1) << 4), fp8_decode8(up ? b.x : b.z, up ? b.y : b.w, c1));
     }
 }
 
@@ -311,27 +302,27 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
     const int heads = a.Hq - h0 < NH ? a.Hq - h0 : NH;
     const int64_t rbase = b * a.t_max;
 
-    // the share's last slot that counts bounds the walk (a share of one tile is
-    // walked as it is)
-    const int32_t count_all = hi - lo <= kTile ? 1 : 0;
+    // The walk goes as far as the share's last slot that counts, and over one
+    // tile at least (a share of one tile is not looked through).
+    const bool one_tile = hi - lo <= kTile;
     bool ok = true;
     int tiles = 1;
 
     if (warp < kWork / 32) {
         const int t = threadIdx.x;
-        const int j = t >> 2, h = t & 3;                   // gather: row of the tile, quarter of it
+        // gather: two rows of the tile, 16 bytes of each 128
+        const int p8 = t & 7, j0 = t >> 3, j1 = kTile / 2 + (j0 ^ 1);
         const int q4 = warp & 3, c = warp >> 2;            // softmax: TMEM lane quarter, quarter of the heads
         const bool active = c * kCols < NH;
         const int key = q4 * 32 + lane;
         const uint32_t lane_addr = (uint32_t)(q4 * 32) << 16;
         const int dqk = a.dc + a.dr;
-        auto row_of = [&](int i) {                         // this thread's row of tile i
+        auto row_of = [&](int i, int j) {                  // the cache row of tile i's row j
             const int s = lo + i * kTile + j;
             return slot_row(a, list, s < hi ? s : a.slots, limit, done);
         };
-        int32_t trow = row_of(0);
-        RawRow<F> raw;
-        load_raw<F>(raw, a, rbase, trow, h);
+        const int own = p8 < 4 ? j0 : j1;
+        int32_t town = row_of(0, own);
         // the query, as nc + 1 K-major blocks of 64 columns (absent heads and
         // columns are zero-filled)
         const __nv_bfloat16 *q = a.q + (row * a.Hq + h0) * dqk;
@@ -342,16 +333,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
                        q + (v ? head * dqk + blk * 64 + p * 8 : 0), v ? 16u : 0u);
         }
         cp_async_arrive(&ctl.q_full);
-        if (!count_all) {
-            int last = -1;
-            for (int s = lo + t; s < hi; s += kWork)
-                if (slot_row(a, list, s, limit, done) >= 0) last = s;
-            last = __reduce_max_sync(0xffffffffu, last);
-            if (lane == 0 && last >= 0) atomicMax(&ctl.last, last);
-            tc::named_barrier(2, kThreads);
-            tiles = ctl.last < lo ? 0 : (ctl.last - lo) / kTile + 1;
-        }
-        int32_t tnext = tiles > 1 ? row_of(1) : -1;
+        RawRows<F> raw;
+        int32_t t0 = __shfl_sync(0xffffffffu, town, 0, 8), t1 = __shfl_sync(0xffffffffu, town, 4, 8);
+        load_rows<F>(raw, a, rbase, t0, t1, p8);
+        town = row_of(1, own);
         float lsum[kCols];
 #pragma unroll
         for (int e = 0; e < kCols; e++) lsum[e] = 0.f;
@@ -364,33 +349,51 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
                 if (m >= mt) break;
                 if (i > 0 && !tc::mbar_wait(&ctl.o_done[m], (i - 1) & 1, a.err, abort)) ok = false;
                 if constexpr (F == DSA_BF16) {
-                    copy_chunk(a, rbase, trow, 256 * m, tile + 2 * m * kRegion, warp, lane);
-                    copy_chunk(a, rbase, trow, 256 * m + 128, tile + (2 * m + 1) * kRegion, warp, lane);
+                    const int64_t r0 = (rbase + (t0 < 0 ? 0 : t0)) * a.row_bytes + 256 * m + 16 * p8;
+                    const int64_t r1 = (rbase + (t1 < 0 ? 0 : t1)) * a.row_bytes + 256 * m + 16 * p8;
+                    const uint32_t d0 = tile + 2 * m * kRegion + j0 * 128 + ((p8 ^ (j0 & 7)) << 4);
+                    const uint32_t d1 = tile + 2 * m * kRegion + j1 * 128 + ((p8 ^ (j1 & 7)) << 4);
+                    cp_async16(d0, a.kv + r0, t0 < 0 ? 0u : 16u);
+                    cp_async16(d1, a.kv + r1, t1 < 0 ? 0u : 16u);
+                    cp_async16(d0 + kRegion, a.kv + r0 + 128, t0 < 0 ? 0u : 16u);
+                    cp_async16(d1 + kRegion, a.kv + r1 + 128, t1 < 0 ? 0u : 16u);
                     cp_async_arrive(&ctl.full[m]);
                 } else {
-                    store_pair<F>(raw, m, tile, h, j);
-                    tc::fence_proxy_async_smem();
+                    store_pair<F>(raw, m, tile, p8, j0, j1);
                     tc::mbar_arrive(&ctl.full[m]);
                 }
             }
-#pragma unroll
-            for (int p = 0; p < 2; p++) st_shared_v4(pbase + j * 128 + (((2 * h + p) ^ (j & 7)) << 4), raw.rope[p]);
+            st_shared_v4(pbase + j0 * 128 + ((p8 ^ (j0 & 7)) << 4), raw.rope0);
+            st_shared_v4(pbase + j1 * 128 + ((p8 ^ (j1 & 7)) << 4), raw.rope1);
             {
-                // the warp's eight rows: one bit each
-                uint32_t x = __ballot_sync(0xffffffffu, trow >= 0) & 0x11111111u;
-                x = (x | x >> 3) & 0x03030303u;
-                x = (x | x >> 6) & 0x000F000Fu;
-                x = (x | x >> 12) & 0xFFu;
-                if (lane == 0) ctl.valid[i & 1][warp] = (uint8_t)x;
+                // the warp's rows 4 warp .. 4 warp + 3 and those 64 further on
+                const uint32_t x0 = __ballot_sync(0xffffffffu, t0 >= 0), x1 = __ballot_sync(0xffffffffu, t1 >= 0);
+                // (those trade places in pairs)
+                auto pack = [](uint32_t x) { return (x & 1) | (x >> 7 & 2) | (x >> 14 & 4) | (x >> 21 & 8); };
+                if (lane == 0) {
+                    const uint32_t y = pack(x1);
+                    ctl.valid[i & 1][warp] = (uint8_t)pack(x0);
+                    ctl.valid[i & 1][kTile / 8 + warp] = (uint8_t)((y & 5) << 1 | (y >> 1 & 5));
+                }
             }
-            tc::fence_proxy_async_smem();
             tc::mbar_arrive(&ctl.full[4]);
-            trow = tnext;
-            if (i + 1 < tiles) load_raw<F>(raw, a, rbase, trow, h);
-            if (i + 2 < tiles) tnext = row_of(i + 2);
+            t0 = __shfl_sync(0xffffffffu, town, 0, 8);
+            t1 = __shfl_sync(0xffffffffu, town, 4, 8);
+            load_rows<F>(raw, a, rbase, t0, t1, p8);       // (rows past the share's end are -1)
+            town = row_of(i + 2, own);
+            if (i == 0 && !one_tile) {
+                int last = -1;
+#pragma unroll 4
+                for (int s = lo + t; s < hi; s += kWork)
+                    if (slot_row(a, list, s, limit, done) >= 0) last = s;
+                last = __reduce_max_sync(0xffffffffu, last);
+                if (lane == 0 && last >= 0) atomicMax(&ctl.last, last);
+                tc::named_barrier(2, kThreads);
+                tiles = ctl.last < lo ? 1 : (ctl.last - lo) / kTile + 1;
+            }
             if (!tc::mbar_wait(&ctl.s_done, i & 1, a.err, abort)) ok = false;
             tc::tc_fence_after();
-            const bool valid = ctl.valid[i & 1][key >> 3] >> (key & 7) & 1;
+            const bool valid = ctl.valid[i & 1][key >> 2] >> (key & 3) & 1;
             bool over = false;
 #pragma unroll
             for (int x = 0; active && x < kCols; x += kStep) {
@@ -474,7 +477,6 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
                                  make_uint4(pk[0], pk[1], pk[2], pk[3]));
                 }
             }
-            tc::fence_proxy_async_smem();
             tc::tc_fence_before();
             tc::mbar_arrive(&ctl.p_full);
         }
@@ -494,13 +496,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
             else if (a.lse)
                 a.lse[row * a.Hq + h0 + t] = l == 0.f ? -INFINITY : (ctl.ref[t] + log2f(l)) * kLn2;
         }
-        if (!tc::mbar_wait(&ctl.q_full, 0, a.err, abort)) ok = false;   // (own copies, when no tile was walked)
     } else {
         // ------------------------------------------------------------- MMA
-        if (!count_all) {
-            tc::named_barrier(2, kThreads);
-            tiles = ctl.last < lo ? 0 : (ctl.last - lo) / kTile + 1;
-        }
         {
             // (the whole warp walks, one elected lane issues: uniform control
             // keeps the descriptors in uniform registers)
@@ -513,15 +510,18 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
             const uint64_t vd0 = tc::smem_desc(tile, 1024, tc::kSwizzle128B, kRegion);
             const uint64_t pd0 = tc::smem_desc(pbase, 1024, tc::kSwizzle128B, kRegion);
             const int rope_steps = (a.dr + 15) / 16;
-            ok = tiles > 0 && tc::mbar_wait(&ctl.q_full, 0, a.err, abort);
-            tc::fence_proxy_async_smem();                  // the query came by cp.async
+            bool counted = one_tile;
+            ok = tc::mbar_wait(&ctl.q_full, 0, a.err, abort);
+            tc::fence_proxy_async_smem();
             for (int i = 0; ok && i < tiles; i++) {
                 const uint32_t ph = i & 1;
-                // (the threads that store fence before they arrive; behind
-                // cp.async the fence is this thread's)
+                // What is behind the barriers was written through the generic
+                // proxy (stores or cp.async); this warp's fence orders it before
+                // the MMAs' reads (one fence here costs less than one in each
+                // of the storing threads: 1007 against 1020 us at 1024 queries).
                 for (int m = 0; ok && m < mt; m++) {
                     ok = tc::mbar_wait(&ctl.full[m], ph, a.err, abort);
-                    if (F == DSA_BF16) tc::fence_proxy_async_smem();
+                    tc::fence_proxy_async_smem();
                     tc::tc_fence_after();
                     const uint64_t kd = kd0 + m * (2 * kRegion / 16), qd = qd0 + m * (2 * NH * 128 / 16);
                     if (tc::elect_one()) {
@@ -533,6 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
                     __syncwarp();
                 }
                 if (!ok || !(ok = tc::mbar_wait(&ctl.full[4], ph, a.err, abort))) break;
+                tc::fence_proxy_async_smem();
                 tc::tc_fence_after();
                 if (tc::elect_one()) {
                     for (int x = 0; x < rope_steps; x++)
@@ -541,7 +542,13 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
                     tc::tc_commit(&ctl.s_done);
                 }
                 __syncwarp();
+                if (i == 0 && !one_tile) {
+                    tc::named_barrier(2, kThreads);
+                    counted = true;
+                    tiles = ctl.last < lo ? 1 : (ctl.last - lo) / kTile + 1;
+                }
                 if (!(ok = tc::mbar_wait(&ctl.p_full, ph, a.err, abort))) break;
+                tc::fence_proxy_async_smem();
                 tc::tc_fence_after();
                 // step x: slots [16 x, 16 x + 16) of the chunk pair (A, two
                 // 64-column atoms 16 KB apart) and of P (B), both MN-major
@@ -557,6 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
                 }
                 __syncwarp();
             }
+            if (!counted) tc::named_barrier(2, kThreads);   // (a wait gave up before the count)
             // every issued MMA completes before TMEM is released
             if (tc::elect_one()) tc::tc_commit(&ctl.mma_fin);
             __syncwarp();
@@ -570,12 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
         // thread = (column of dc, quarter of the heads): a warp stores 32
         // consecutive columns of one head at a time
         const int q4 = warp & 3, c = warp >> 2;
-        if (tiles == 0) {
-            // nothing selected: zeros (a split's empty partial is its sum of 0)
-            if (a.splits == 1)
-                for (int f = threadIdx.x; f < heads * a.dc / 8; f += kWork)
-                    reinterpret_cast<uint4 *>(a.out + (row * a.Hq + h0) * a.dc)[f] = make_uint4(0, 0, 0, 0);
-        } else if (c * kCols < NH) {
+        if (c * kCols < NH) {
             for (int m = 0; m < mt; m++) {
                 if (!tc::mbar_wait(&ctl.o_done[m], (tiles - 1) & 1, a.err, abort)) ok = false;
                 tc::tc_fence_after();
@@ -606,38 +609,54 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
     }
 }
 
-// Merges a row's splits: thread = four output columns of one head.
+// Merges a row's splits: block = one head of one row, thread = four output
+// columns.
 //   M = max_s ref_s,  out = sum_s 2^(ref_s - M) O_s / sum_s 2^(ref_s - M) l_s
+// Every warp works the splits' weights out for itself (lane = split), so that
+// the partials' loads depend on two loads and no barrier; eight are in flight.
 __global__ void __launch_bounds__(128)
 latent_combine_kernel(const float *part_o, const float2 *part_ml, int splits, int groups, int nh, int Hq, int dc,
                       __nv_bfloat16 *out, float *lse) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t row = blockIdx.x / (unsigned)Hq;
-    const int head = (int)(blockIdx.x % (unsigned)Hq);
+    const int head = (int)(blockIdx.x % (unsigned)Hq), lane = threadIdx.x & 31;
     const int64_t unit = (row * groups + head / kMaxHeads) * splits;
-    const int hd = head % kMaxHeads;
+    const float2 *ml = part_ml + unit * nh + head % kMaxHeads;
+    const float4 *o = reinterpret_cast<const float4 *>(part_o + (unit * nh + head % kMaxHeads) * dc) + threadIdx.x;
+    const int64_t step = (int64_t)nh * dc / 4;             // float4s from split to split
     float M = -INFINITY;
-    for (int s = 0; s < splits; s++) M = fmaxf(M, part_ml[(unit + s) * nh + hd].x);
+    for (int s = lane; s < splits; s += 32) M = fmaxf(M, ml[(int64_t)s * nh].x);
+    M = warp_max(M);
     float L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int s = 0; s < splits; s++) {
-        const float2 ml = part_ml[(unit + s) * nh + hd];
-        if (ml.y == 0.f) continue;                         // an empty share wrote no partial
-        const float w = ml.x == M ? 1.f : ex2(ml.x - M);
-        L = fmaf(w, ml.y, L);
-        const float4 o = reinterpret_cast<const float4 *>(part_o + ((unit + s) * nh + hd) * dc)[threadIdx.x];
-        acc.x = fmaf(w, o.x, acc.x);
-        acc.y = fmaf(w, o.y, acc.y);
-        acc.z = fmaf(w, o.z, acc.z);
-        acc.w = fmaf(w, o.w, acc.w);
+    for (int s0 = 0; s0 < splits; s0 += 32) {
+        // an empty share has l = 0 and wrote no partial: weight 0, not read
+        const float2 v = s0 + lane < splits ? ml[(int64_t)(s0 + lane) * nh] : make_float2(-INFINITY, 0.f);
+        const float w = v.y == 0.f ? 0.f : v.x == M ? 1.f : ex2(v.x - M);
+        const uint32_t live = __ballot_sync(0xffffffffu, v.y != 0.f);
+        L += warp_sum(w == 0.f ? 0.f : w * v.y);
+        const int n = splits - s0 < 32 ? splits - s0 : 32;
+        for (int s1 = 0; s1 < n; s1 += 8) {
+            float4 x[8];
+#pragma unroll
+            for (int u = 0; u < 8; u++)
+                x[u] = live >> (s1 + u) & 1 ? o[(s0 + s1 + u) * step] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int u = 0; u < 8; u++) {
+                const float wu = __shfl_sync(0xffffffffu, w, s1 + u);
+                acc.x = fmaf(wu, x[u].x, acc.x);
+                acc.y = fmaf(wu, x[u].y, acc.y);
+                acc.z = fmaf(wu, x[u].z, acc.z);
+                acc.w = fmaf(wu, x[u].w, acc.w);
+            }
+        }
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
-    uint2 w;
-    w.x = bf16x2_bits(__floats2bfloat162_rn(acc.x * inv, acc.y * inv));
-    w.y = bf16x2_bits(__floats2bfloat162_rn(acc.z * inv, acc.w * inv));
-    reinterpret_cast<uint2 *>(out + (row * Hq + head) * dc)[threadIdx.x] = w;
+    uint2 w2;
+    w2.x = bf16x2_bits(__floats2bfloat162_rn(acc.x * inv, acc.y * inv));
+    w2.y = bf16x2_bits(__floats2bfloat162_rn(acc.z * inv, acc.w * inv));
+    reinterpret_cast<uint2 *>(out + (row * Hq + head) * dc)[threadIdx.x] = w2;
     if (threadIdx.x == 0 && lse) lse[row * Hq + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
