@@ -66,6 +66,7 @@ def read(L, **kw):
     (dict(sp=1), INVALID), (dict(sp=-1), INVALID), (dict(n=-1), INVALID), (dict(B=-1), INVALID),
     (dict(cache=NULL), INVALID), (dict(out=NULL), INVALID), (dict(out=ODD), INVALID), (dict(cache=ODD), INVALID),
     (dict(idx=ctypes.c_void_p((1 << 20) + 2)), INVALID),
+    (dict(idx=FAKE, t_max=0), INVALID),
     (dict(n=0, cache=NULL, out=NULL), OK), (dict(B=0, cache=NULL, out=NULL), OK),
 ])
 def test_read_checks(dsa, kw, status):

@@ -7,10 +7,22 @@
 // the cache write) and the diagram "DeepSeek Sparse Attention, one decode step
 // in one layer (V3.2 sizes)" (the FP8 row).
 //
-// Both kernels move bytes: a warp owns a row, a lane eight consecutive latent
-// values at a time (one 16-byte bf16 load, one word of 4-bit codes), so that a
-// row's loads and stores are whole lines, and four lanes hold a 4-bit group,
-// sixteen an FP8 block: their maxima are two or four shuffles.
+// Both kernels move bytes.  The bytes of a row (1152 read and 416 written from
+// bf16 to 4 bits) leave about 270 warp instructions at the memory's rate, so
+// in the prologue half a warp owns a row and a lane 32 consecutive latent values,
+// one 4-bit group: the group's maximum and scale need no exchange and are worked
+// out once per 32 values, the codes leave as one 16-byte store, arithmetic is
+// packed in pairs, a word of codes is put together by multiply-adds on the bits
+// of the rounded quotients, and the next row is loaded ahead.  The read has a
+// warp per row and eight values a lane, so that its wide stores are whole lines.
+//
+// Rounding.  What is stored is the rounding of the exact value (of the products
+// and the norm taken in 64 bits): the fp32 result is used where its error leaves
+// the rounded value in no doubt, and a row (or a rotary pair) where it might not,
+// about three 4-bit rows in a thousand, is taken again in 64 bits.  (FP8 codes of
+// a normed row are rounded from fp32.)
+#include <algorithm>
+
 #include "latent_rows.cuh"
 #include "quant.cuh"
 
@@ -18,7 +30,10 @@ namespace dsa {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kSlots = 2;      // chunks of eight latent values a lane may hold: dc <= 512
+constexpr int kSlots = 2;      // the read's chunks of eight latent values a lane: dc <= 512
+constexpr int kProWarps = 4;   // warps per prologue block (four blocks an SM: registers for a row ahead)
+constexpr int kProBlocks = 4;
+constexpr int kVals = 32;      // the prologue's latent values a lane: half a warp holds dc <= 512
 
 struct PrologueArgs {
     const void *kv;
@@ -33,210 +48,458 @@ struct PrologueArgs {
     int S, dc, dr;
 };
 
-template <typename T>
-__device__ __forceinline__ void load8(const T *p, float (&v)[8]) {
-    if constexpr (sizeof(T) == 2) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const float2 f = bf16x2_to_f32(ws[i]);
-            v[2 * i] = f.x;
-            v[2 * i + 1] = f.y;
-        }
-    } else {
-        const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+// A row number as (sequence, token of n): stepped without a division per row.
+template <typename I>
+struct RowPos {
+    I b, s, step_b, step_s, n;
+    __device__ RowPos(int64_t row, int64_t step, I n) : n(n) {
+        b = (I)(row / n);
+        s = (I)(row - (int64_t)b * n);
+        step_b = (I)(step / n);
+        step_s = (I)(step - (int64_t)step_b * n);
     }
+    __device__ void next() {
+        b += step_b;
+        // (s < n and step_s < n; the sum may pass the type's range)
+        const bool over = s >= n - step_s;
+        s = over ? s - (n - step_s) : s + step_s;
+        b += over;
+    }
+};
+
+// A lane's 32 latent values and four rotary ones as they lie in memory.
+template <typename T> struct RawRow;
+template <> struct RawRow<__nv_bfloat16> {
+    using Vec = uint4;
+    using Pair = uint32_t;
+    uint4 c[4];
+    uint32_t pe[2];
+};
+template <> struct RawRow<float> {
+    using Vec = float4;
+    using Pair = float2;
+    float4 c[8];
+    float2 pe[2];
+};
+
+__device__ __forceinline__ void widen(const RawRow<__nv_bfloat16> &r, float2 (&x)[kVals / 2], float2 (&pe)[2]) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        x[4 * i] = bf16x2_to_f32(r.c[i].x);
+        x[4 * i + 1] = bf16x2_to_f32(r.c[i].y);
+        x[4 * i + 2] = bf16x2_to_f32(r.c[i].z);
+        x[4 * i + 3] = bf16x2_to_f32(r.c[i].w);
+    }
+    pe[0] = bf16x2_to_f32(r.pe[0]);
+    pe[1] = bf16x2_to_f32(r.pe[1]);
+}
+__device__ __forceinline__ void widen(const RawRow<float> &r, float2 (&x)[kVals / 2], float2 (&pe)[2]) {
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        x[2 * i] = make_float2(r.c[i].x, r.c[i].y);
+        x[2 * i + 1] = make_float2(r.c[i].z, r.c[i].w);
+    }
+    pe[0] = r.pe[0];
+    pe[1] = r.pe[1];
+}
+
+// max |a|, |b| that a NaN passes through: a group holding one gets a NaN scale
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
+
+// The 4-bit word of eight quotients: adding 1.5 * 2^23 + 8 rounds each to the
+// nearest integer n (ties to even) and leaves n + 8 in the low bits on top of a
+// constant, which the sum of the shifted words carries off.
+constexpr float kMagic = 12582912.f + 8.f;
+constexpr uint32_t kMagicBits = 0x4B400000u;        // of 1.5 * 2^23
+__device__ __forceinline__ uint32_t q4_word(const float2 *r) {          // four pairs of quotients + kMagic
+    uint32_t w = 0u - kMagicBits * 0x11111111u;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        w += __float_as_uint(r[i].x) << (4 * i);
+        w += __float_as_uint(r[i].y) << (4 * (i + 4));
+    }
+    return w;
+}
+
+// A latent row's rounding in 64 bits, by the whole warp: lane = values lane,
+// lane + 32, ... (a 4-bit group at a time).  It runs for few rows; a function of
+// its own keeps its registers out of the common path.
+template <int F, typename T>
+__device__ __noinline__ void exact_row(const T *src, uint8_t *dst, const float *w, float eps, int dc, int dr) {
+    const int lane = threadIdx.x & 31;
+    double x[16], ss = 0.0;
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+        x[i] = 32 * i < dc ? (double)to_f32<T>(src[32 * i + lane]) : 0.0;
+        ss = fma(x[i], x[i], ss);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const double r = 1.0 / sqrt(ss / dc + (double)eps);
+#pragma unroll 4
+    for (int i = 0; i < 16; i++) {
+        if (32 * i >= dc) break;
+        const int d = 32 * i + lane;
+        const double y = x[i] * r * (double)w[d];
+        if constexpr (F == DSA_Q4_LATENT) {
+            double amax = fabs(y);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) amax = fmax(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            const __nv_bfloat16 sb = __float2bfloat16_rn(__double2float_rn(fmax(amax, (double)1e-4f) / 7.0));
+            const int v = d & 7;
+            uint32_t code = (uint32_t)(8 + __double2int_rn(y / (double)__bfloat162float(sb))) << (4 * (v / 2 + 4 * (v & 1)));
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) code |= __shfl_xor_sync(0xffffffffu, code, o);
+            if (v == 0) reinterpret_cast<uint32_t *>(dst)[d >> 3] = code;
+            if (lane == 0) reinterpret_cast<__nv_bfloat16 *>(dst + latent_q4_scales_at(dc, dr))[d >> 5] = sb;
+        } else {
+            reinterpret_cast<__nv_bfloat16 *>(dst)[d] = __float2bfloat16_rn(__double2float_rn(y));
+        }
+    }
+}
+
+// The rotation of one pair (re, im) by (cos, sin), as bf16.
+__device__ __forceinline__ __nv_bfloat162 rotate_bf16(float re, float im, float2 cs) {
+    const float a = re * cs.x, b = im * cs.y, c = re * cs.y, d = im * cs.x;
+    const float y0 = a - b, y1 = c + d;
+    // three roundings each, of terms this large
+    const float e0 = (fabsf(a) + fabsf(b)) * 0x1p-22f, e1 = (fabsf(c) + fabsf(d)) * 0x1p-22f;
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(y0 - e0, y1 - e1), hi = __floats2bfloat162_rn(y0 + e0, y1 + e1);
+    if (bf16x2_bits(lo) == bf16x2_bits(hi)) return lo;
+    const double z0 = (double)re * cs.x - (double)im * cs.y, z1 = (double)re * cs.y + (double)im * cs.x;
+    return __floats2bfloat162_rn(__double2float_rn(z0), __double2float_rn(z1));
 }
 
 // Row r = (b, s): y = c * rsqrt(mean(c^2) + eps) * w (without norm_w, y = c),
-// k_pe times the position's (cos, sin), then the format's rounding.  Sums and
-// products stay in fp32 until that one rounding.
+// k_pe times the position's (cos, sin), then the format's rounding.
 template <int F, typename T>
-__global__ void __launch_bounds__(32 * kWarps)
-latent_prologue_kernel(const PrologueArgs a) {
-    const int lane = threadIdx.x & 31;
-    const int chunks = a.dc / 8;
-    const int64_t rb = latent_fmt_row_bytes(F, a.dc, a.dr);
-    float w[kSlots][8];
-    if (a.norm_w) {
-#pragma unroll
-        for (int u = 0; u < kSlots; u++)
-            if (lane + 32 * u < chunks) load8(a.norm_w + 8 * (lane + 32 * u), w[u]);
+__global__ void __launch_bounds__(32 * kProWarps, kProBlocks) latent_prologue_kernel(const PrologueArgs a) {
+    // the norm's weights, a lane's 32 at a pitch that keeps lanes off each
+    // other's banks
+    constexpr int kPitch = kVals + 4;
+    __shared__ float4 w_sm[16 * kPitch / 4], w_flat[512 / 4];
+    const int lane = threadIdx.x & 31, l16 = lane & 15;
+    const bool norm = a.norm_w != nullptr;
+    static_assert(32 * kProWarps >= 512 / 4, "one load fills the weights");
+    if (norm && threadIdx.x < a.dc / 4) {
+        const float4 v = reinterpret_cast<const float4 *>(a.norm_w)[threadIdx.x];
+        w_flat[threadIdx.x] = v;
+        w_sm[(threadIdx.x / 8) * (kPitch / 4) + threadIdx.x % 8] = v;
     }
-    const int64_t step = (int64_t)gridDim.x * kWarps;
-    for (int64_t r = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); r < a.rows; r += step) {
-        const int64_t b = r / a.S, s = r - b * a.S;
-        const T *src = static_cast<const T *>(a.kv) + b * a.batch_stride + s * a.token_stride;
-        uint8_t *dst = a.cache + (b * a.t_max + a.start_pos + s) * rb;
-        float x[kSlots][8];
+    __syncthreads();
+    const int64_t rb = latent_fmt_row_bytes(F, a.dc, a.dr);
+    const float inv_dc = 1.f / (float)a.dc;
+    const bool has_c = kVals * l16 < a.dc;
+    // rotary pairs 2 l and 2 l + 1: elements 4 l .. 4 l + 3, or, when the
+    // embedding is not interleaved, 2 l, 2 l + 1 and those dr/2 further on
+    const int half = a.dr / 2;
+    const bool has_pe = 4 * l16 < a.dr, halves = a.rope_cs && !a.interleaved;
+    const int e0 = halves ? 2 * l16 : 4 * l16, e1 = halves ? 2 * l16 + half : 4 * l16 + 2;
+
+    RawRow<T> raw = {};
+    float4 cs = make_float4(1.f, 0.f, 1.f, 0.f);
+    auto source = [&](int b, int s) {
+        return static_cast<const T *>(a.kv) + b * a.batch_stride + s * a.token_stride;
+    };
+    auto fetch = [&](int b, int s) {
+        const T *src = source(b, s);
+        if (has_c) {
+            constexpr int n = sizeof(raw.c) / 16;
 #pragma unroll
-        for (int u = 0; u < kSlots; u++) {
-            if (lane + 32 * u < chunks) {
-                load8(src + 8 * (lane + 32 * u), x[u]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; e++) x[u][e] = 0.f;
-            }
+            for (int i = 0; i < n; i++) raw.c[i] = reinterpret_cast<const typename RawRow<T>::Vec *>(src + kVals * l16)[i];
         }
-        // the rotary pair of this lane: elements (2l, 2l + 1), or (l, l + dr/2)
-        // when the embedding is not interleaved
-        const int half = a.dr / 2;
-        const bool has_pe = lane < half;
-        const bool halves = a.rope_cs && !a.interleaved;
-        const int e0 = halves ? lane : 2 * lane, e1 = halves ? lane + half : 2 * lane + 1;
-        float p0 = 0.f, p1 = 0.f;
         if (has_pe) {
-            p0 = to_f32<T>(src[a.dc + e0]);
-            p1 = to_f32<T>(src[a.dc + e1]);
-            if (a.rope_cs) {
-                const float2 cs = reinterpret_cast<const float2 *>(a.rope_cs)[s * half + lane];
-                const float y0 = __fsub_rn(__fmul_rn(p0, cs.x), __fmul_rn(p1, cs.y));
-                p1 = __fadd_rn(__fmul_rn(p0, cs.y), __fmul_rn(p1, cs.x));
-                p0 = y0;
+            raw.pe[0] = *reinterpret_cast<const typename RawRow<T>::Pair *>(src + a.dc + e0);
+            raw.pe[1] = *reinterpret_cast<const typename RawRow<T>::Pair *>(src + a.dc + e1);
+            if (a.rope_cs) cs = reinterpret_cast<const float4 *>(a.rope_cs + (int64_t)s * a.dr)[l16];
+        }
+    };
+    // a warp's two rows: 2 k and 2 k + 1
+    const int64_t step = 2 * (int64_t)gridDim.x * kProWarps;
+    int64_t r = 2 * ((int64_t)blockIdx.x * kProWarps + (threadIdx.x >> 5)) + (lane >> 4);
+    RowPos<int> at(r, step, a.S);
+    if (r < a.rows) fetch(at.b, at.s);
+    for (; r - (lane >> 4) < a.rows; r += step) {
+        const bool on = r < a.rows;
+        const int b = at.b, s = at.s;
+        uint8_t *dst = a.cache + (b * a.t_max + a.start_pos + s) * rb;
+        float2 x[kVals / 2], pe[2];
+        widen(raw, x, pe);
+        const float4 cs_now = cs;
+        at.next();
+        if (r + step < a.rows) fetch(at.b, at.s);
+
+        float rms = 1.f;
+        if (norm) {
+            float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+#pragma unroll
+            for (int e = 0; e < kVals / 2; e += 2) {
+                s0 = __ffma2_rn(x[e], x[e], s0);
+                s1 = __ffma2_rn(x[e + 1], x[e + 1], s1);
+            }
+            float ss = (s0.x + s0.y) + (s1.x + s1.y);
+#pragma unroll
+            for (int m = 8; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+            const float v = fmaf(ss, inv_dc, a.eps);
+            rms = rsqrtf(v);
+            rms = fmaf(rms * 0.5f, fmaf(-v * rms, rms, 1.f), rms);      // a Newton step: within a rounding or two
+#pragma unroll
+            for (int e = 0; e < kVals / 4; e++) {
+                const float4 wv = w_sm[l16 * (kPitch / 4) + e];
+                // the norm's factor comes later
+                x[2 * e] = __fmul2_rn(x[2 * e], make_float2(wv.x, wv.y));
+                x[2 * e + 1] = __fmul2_rn(x[2 * e + 1], make_float2(wv.z, wv.w));
             }
         }
-        if (a.norm_w) {
-            float ss = 0.f;
+        bool doubt = false;
+        if constexpr (F == DSA_BF16) {
 #pragma unroll
-            for (int u = 0; u < kSlots; u++)
-#pragma unroll
-                for (int e = 0; e < 8; e++) ss = fmaf(x[u][e], x[u][e], ss);
-            const float rms = __frcp_rn(__fsqrt_rn(warp_sum(ss) / (float)a.dc + a.eps));
-#pragma unroll
-            for (int u = 0; u < kSlots; u++)
-                if (lane + 32 * u < chunks)
-#pragma unroll
-                    for (int e = 0; e < 8; e++) x[u][e] = x[u][e] * rms * w[u][e];
-        }
-#pragma unroll
-        for (int u = 0; u < kSlots; u++) {
-            const int chunk = lane + 32 * u;
-            if (F != DSA_BF16) {
-                // (every lane takes part in the shuffles; a group lies within one u)
-                float amax = 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; e++) amax = fmaxf(amax, fabsf(x[u][e]));
-#pragma unroll
-                for (int m = 1; m < (F == DSA_FP8_LATENT ? 16 : 4); m <<= 1)
-                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
-                amax = fmaxf(amax, 1e-4f);
-                if (chunk < chunks) {
-                    if constexpr (F == DSA_FP8_LATENT) {
-                        const float sc = __fdiv_rn(amax, 448.0f), rs = __frcp_rn(sc);
-                        uint32_t c[4];
-#pragma unroll
-                        for (int e = 0; e < 4; e++)
-                            c[e] = e4m3x2_rn_sat(div_rn_by(x[u][2 * e], sc, rs), div_rn_by(x[u][2 * e + 1], sc, rs));
-                        // (rows of some shapes are only 4-byte aligned)
-                        reinterpret_cast<uint32_t *>(dst)[2 * chunk] = c[0] | c[1] << 16;
-                        reinterpret_cast<uint32_t *>(dst)[2 * chunk + 1] = c[2] | c[3] << 16;
-                        if ((chunk & 15) == 0) reinterpret_cast<float *>(dst + a.dc)[chunk >> 4] = sc;
-                    } else {
-                        const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(amax, 7.0f));
-                        const float sc = __bfloat162float(sb), rs = __frcp_rn(sc);
-                        uint32_t c = 0;
-#pragma unroll
-                        for (int e = 0; e < 8; e++) {
-                            const int n = max(-7, min(7, __float2int_rn(div_rn_by(x[u][e], sc, rs))));
-                            c |= (uint32_t)(n + 8) << (4 * (e / 2 + 4 * (e & 1)));
-                        }
-                        reinterpret_cast<uint32_t *>(dst)[chunk] = c;
-                        if ((chunk & 3) == 0)
-                            reinterpret_cast<__nv_bfloat16 *>(dst + latent_q4_scales_at(a.dc, a.dr))[chunk >> 2] = sb;
-                    }
-                }
-            } else if (chunk < chunks) {
+            for (int i = 0; i < 4; i++) {
                 uint32_t c[4];
 #pragma unroll
-                for (int e = 0; e < 4; e++) c[e] = bf16x2_bits(__floats2bfloat162_rn(x[u][2 * e], x[u][2 * e + 1]));
-                reinterpret_cast<uint4 *>(dst)[chunk] = make_uint4(c[0], c[1], c[2], c[3]);
+                for (int e = 0; e < 4; e++) {
+                    const float2 y = __fmul2_rn(x[4 * i + e], splat(rms));
+                    c[e] = bf16x2_bits(__floats2bfloat162_rn(y.x, y.y));
+                    // the part below bf16 within 4 of 2^16 units of the middle
+                    doubt |= ((__float_as_uint(y.x) + 0x8004u) & 0xFFFFu) < 8u || ((__float_as_uint(y.y) + 0x8004u) & 0xFFFFu) < 8u;
+                }
+                if (on && has_c) reinterpret_cast<uint4 *>(dst)[4 * l16 + i] = make_uint4(c[0], c[1], c[2], c[3]);
+            }
+        } else {
+            float amax = 0.f;
+#pragma unroll
+            for (int e = 0; e < kVals / 2; e++) amax = max_nan(amax, max_nan(fabsf(x[e].x), fabsf(x[e].y)));
+            if constexpr (F == DSA_FP8_LATENT) {
+                // a block of 128 is four lanes'
+                amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                const float sc = div_rn_by(fmaxf(amax * rms, 1e-4f), 448.0f, 1.0f / 448.0f), rs = __frcp_rn(sc);
+                const float2 rs2 = splat(rs), ns2 = splat(-sc);
+                uint32_t words[kVals / 4];
+#pragma unroll
+                for (int i = 0; i < kVals / 4; i++) {
+                    uint32_t c[2];
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {          // the correctly rounded quotient (div_rn_by, in pairs)
+                        const float2 y = __fmul2_rn(x[2 * i + e], splat(rms));
+                        const float2 q0 = __fmul2_rn(y, rs2);
+                        const float2 q = __ffma2_rn(__ffma2_rn(q0, ns2, y), rs2, q0);
+                        c[e] = e4m3x2_rn_sat(q.x, q.y);
+                    }
+                    words[i] = c[0] | c[1] << 16;
+                }
+                if (on && has_c) {
+                    if ((rb & 15) == 0) {
+                        reinterpret_cast<uint4 *>(dst)[2 * l16] = make_uint4(words[0], words[1], words[2], words[3]);
+                        reinterpret_cast<uint4 *>(dst)[2 * l16 + 1] = make_uint4(words[4], words[5], words[6], words[7]);
+                    } else {                   // (rows of shapes other than 512 are only 4-byte aligned)
+#pragma unroll
+                        for (int i = 0; i < kVals / 4; i++) reinterpret_cast<uint32_t *>(dst)[8 * l16 + i] = words[i];
+                    }
+                }
+                if (on && has_c && (l16 & 3) == 0) reinterpret_cast<float *>(dst + a.dc)[l16 >> 2] = sc;
+            } else {
+                const float st = div_rn_by(max_nan(amax * rms, 1e-4f), 7.0f, 1.0f / 7.0f);
+                const __nv_bfloat16 sb = __float2bfloat16_rn(st);
+                const float sc = __bfloat162float(sb), rs = __frcp_rn(sc);
+                if (norm) {
+                    // in doubt: a quotient (seven at most, a few roundings off)
+                    // within 2^-19 of a border, a scale within 2 of 2^16 units
+                    const float2 k = splat(rms * rs);
+                    float far = 0.f;
+#pragma unroll
+                    for (int e = 0; e < kVals / 2; e++) {
+                        const float2 q = __fmul2_rn(x[e], k);
+                        x[e] = __fadd2_rn(q, splat(kMagic));
+                        const float2 n = __fadd2_rn(x[e], splat(-kMagic));
+                        const float2 d = __ffma2_rn(q, splat(-1.f), n);
+                        far = fmaxf(far, fmaxf(fabsf(d.x), fabsf(d.y)));
+                    }
+                    doubt = far > 0.5f - 0x1p-19f || ((__float_as_uint(st) + 0x8002u) & 0xFFFFu) < 4u;
+                } else {
+                    const float2 rs2 = splat(rs), ns2 = splat(-sc);
+#pragma unroll
+                    for (int e = 0; e < kVals / 2; e++) {  // the correctly rounded quotient
+                        const float2 q0 = __fmul2_rn(x[e], rs2);
+                        x[e] = __fadd2_rn(__ffma2_rn(__ffma2_rn(q0, ns2, x[e]), rs2, q0), splat(kMagic));
+                    }
+                }
+                if (on && has_c) {
+                    reinterpret_cast<uint4 *>(dst)[l16] = make_uint4(q4_word(x), q4_word(x + 4), q4_word(x + 8), q4_word(x + 12));
+                    reinterpret_cast<__nv_bfloat16 *>(dst + latent_q4_scales_at(a.dc, a.dr))[l16] = sb;
+                }
             }
         }
-        if (has_pe) {
-            __nv_bfloat16 *pe = reinterpret_cast<__nv_bfloat16 *>(dst + latent_rope_at<F>(a.dc));
-            pe[e0] = __float2bfloat16_rn(p0);
-            pe[e1] = __float2bfloat16_rn(p1);
+        if (F != DSA_FP8_LATENT && norm) {
+            const uint32_t rows = __ballot_sync(0xffffffffu, doubt && on && has_c);
+            if (rows) {
+                __syncwarp();                              // the fp32 result's stores come first
+#pragma unroll 1
+                for (int h = 0; h < 2; h++) {
+                    if (!(rows >> (16 * h) & 0xFFFFu)) continue;
+                    const int hb = __shfl_sync(0xffffffffu, b, 16 * h), hs = __shfl_sync(0xffffffffu, s, 16 * h);
+                    exact_row<F, T>(source(hb, hs), a.cache + (hb * a.t_max + a.start_pos + hs) * rb,
+                                    reinterpret_cast<const float *>(w_flat), a.eps, a.dc, a.dr);
+                }
+            }
+        }
+        if (on && has_pe) {
+            __nv_bfloat162 *out = reinterpret_cast<__nv_bfloat162 *>(dst + latent_rope_at<F>(a.dc));
+            if (halves) {
+                const __nv_bfloat162 y0 = rotate_bf16(pe[0].x, pe[1].x, make_float2(cs_now.x, cs_now.y));
+                const __nv_bfloat162 y1 = rotate_bf16(pe[0].y, pe[1].y, make_float2(cs_now.z, cs_now.w));
+                out[e0 / 2] = __halves2bfloat162(y0.x, y1.x);
+                out[e1 / 2] = __halves2bfloat162(y0.y, y1.y);
+            } else {
+                out[e0 / 2] = a.rope_cs ? rotate_bf16(pe[0].x, pe[0].y, make_float2(cs_now.x, cs_now.y)) : __floats2bfloat162_rn(pe[0].x, pe[0].y);
+                out[e1 / 2] = a.rope_cs ? rotate_bf16(pe[1].x, pe[1].y, make_float2(cs_now.z, cs_now.w)) : __floats2bfloat162_rn(pe[1].x, pe[1].y);
+            }
         }
         if (F == DSA_Q4_LATENT) {              // the row's end: zeros up to its pitch
-            const int at = latent_q4_scales_at(a.dc, a.dr) + a.dc / 16;
-            if (at + 2 * lane < rb) *reinterpret_cast<uint16_t *>(dst + at + 2 * lane) = 0;
+            const int end = latent_q4_scales_at(a.dc, a.dr) + a.dc / 16 + 2 * l16;
+            if (on && end < rb) *reinterpret_cast<uint16_t *>(dst + end) = 0;
         }
     }
 }
 
-// Row i of the output = cache row idx[i] (zeros for -1) or start_pos + i.
-template <int F, typename T>
+// A lane's share of a row as it lies in the cache, and its values.
+template <int F> struct RawRead;
+template <> struct RawRead<DSA_BF16> { uint4 c[kSlots]; };
+template <> struct RawRead<DSA_FP8_LATENT> { uint2 c[kSlots]; float s[kSlots]; };
+template <> struct RawRead<DSA_Q4_LATENT> { uint32_t c[kSlots]; __nv_bfloat16 s[kSlots]; };
+
+template <int F>
+__device__ __forceinline__ void read_raw(RawRead<F> &r, const uint8_t *row, int u, int chunk, int dc, int dr) {
+    if constexpr (F == DSA_BF16) {
+        r.c[u] = reinterpret_cast<const uint4 *>(row)[chunk];
+    } else if constexpr (F == DSA_FP8_LATENT) {
+        // (rows of some shapes are only 4-byte aligned)
+        const uint32_t *c = reinterpret_cast<const uint32_t *>(row) + 2 * chunk;
+        r.c[u] = make_uint2(c[0], c[1]);
+        r.s[u] = *reinterpret_cast<const float *>(row + dc + 4 * (chunk >> 4));
+    } else {
+        r.c[u] = reinterpret_cast<const uint32_t *>(row)[chunk];
+        r.s[u] = *reinterpret_cast<const __nv_bfloat16 *>(row + latent_q4_scales_at(dc, dr) + 2 * (chunk >> 2));
+    }
+}
+template <int F>
+__device__ __forceinline__ uint4 read_values(const RawRead<F> &r, int u) {
+    if constexpr (F == DSA_BF16)
+        return r.c[u];
+    else if constexpr (F == DSA_FP8_LATENT)
+        return fp8_decode8(r.c[u].x, r.c[u].y, r.s[u]);
+    else
+        return q4_decode8(r.c[u], __halves2bfloat162(r.s[u], r.s[u]));
+}
+
+// Row i of the output = cache row idx[i] (zeros for -1) or start_pos + i.  A
+// warp takes kRows rows at a time, all their loads before the first decoding
+// (an absent row's or chunk's loads go to row 0 or chunk 0 and are not used).
+template <int F, typename T, int kRows>
 __global__ void __launch_bounds__(32 * kWarps)
 latent_read_kernel(const uint8_t *__restrict__ cache, int64_t t_max, const int32_t *__restrict__ idx,
-                   int64_t start_pos, int64_t rows, int64_t n, int dc, int dr, T *__restrict__ out,
-                   int *err) {
+                   int64_t start_pos, int64_t rows, int64_t n, int dc, int dr, T *__restrict__ out, int *err) {
     const int lane = threadIdx.x & 31;
     const int chunks = dc / 8;
     const int64_t rb = latent_fmt_row_bytes(F, dc, dr);
-    const int64_t step = (int64_t)gridDim.x * kWarps;
-    for (int64_t r = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); r < rows; r += step) {
-        const int64_t b = r / n;
-        int64_t t = idx ? (int64_t)idx[r] : start_pos + (r - b * n);
-        if (t >= t_max) {
-            if (lane == 0) record_error(err, DSA_ERR_DEVICE);
-            t = -1;
-        }
-        const uint8_t *row = cache + (b * t_max + (t < 0 ? 0 : t)) * rb;
-        T *dst = out + r * (dc + dr);
+    const int64_t step = (int64_t)gridDim.x * kWarps * kRows;
+    int64_t r0 = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * kRows;
+    if (r0 >= rows) return;
+    for (RowPos<int64_t> at(r0, step, n); r0 < rows; r0 += step, at.next()) {
+        int64_t t[kRows], b = at.b, s = at.s;
 #pragma unroll
-        for (int u = 0; u < kSlots; u++) {
-            const int chunk = lane + 32 * u;
-            if (chunk >= chunks) continue;
-            const uint4 v = t < 0 ? make_uint4(0, 0, 0, 0) : latent_chunk8<F>(row, dc, dr, chunk);
-            if constexpr (sizeof(T) == 2) {
-                reinterpret_cast<uint4 *>(dst)[chunk] = v;
-            } else {
-                const float2 f0 = bf16x2_to_f32(v.x), f1 = bf16x2_to_f32(v.y), f2 = bf16x2_to_f32(v.z),
-                             f3 = bf16x2_to_f32(v.w);
-                reinterpret_cast<float4 *>(dst)[2 * chunk] = make_float4(f0.x, f0.y, f1.x, f1.y);
-                reinterpret_cast<float4 *>(dst)[2 * chunk + 1] = make_float4(f2.x, f2.y, f3.x, f3.y);
+        for (int i = 0; i < kRows; i++) {
+            if (i > 0 && r0 + i < rows && ++s >= n) {      // (a row past the end is the last one again)
+                s = 0;
+                b++;
             }
+            t[i] = idx ? (int64_t)idx[b * n + s] : start_pos + s;
+            if (t[i] >= t_max && lane == 0) record_error(err, DSA_ERR_DEVICE);
+            t[i] = t[i] < 0 || t[i] >= t_max ? -1 : b * t_max + t[i];
         }
-        if (lane < dr / 2) {
-            const uint32_t v = t < 0 ? 0u : reinterpret_cast<const uint32_t *>(row + latent_rope_at<F>(dc))[lane];
-            if constexpr (sizeof(T) == 2)
-                reinterpret_cast<uint32_t *>(dst + dc)[lane] = v;
-            else
-                reinterpret_cast<float2 *>(dst + dc)[lane] = bf16x2_to_f32(v);
+        RawRead<F> raw[kRows];
+        uint32_t pe[kRows];
+#pragma unroll
+        for (int i = 0; i < kRows; i++) {
+            const uint8_t *row = cache + (t[i] < 0 ? 0 : t[i]) * rb;
+#pragma unroll
+            for (int u = 0; u < kSlots; u++)
+                read_raw<F>(raw[i], row, u, lane + 32 * u < chunks ? lane + 32 * u : 0, dc, dr);
+            pe[i] = dr ? reinterpret_cast<const uint32_t *>(row + latent_rope_at<F>(dc))[lane < dr / 2 ? lane : 0] : 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; i++) {
+            if (r0 + i >= rows) break;
+            T *dst = out + (r0 + i) * (dc + dr);
+#pragma unroll
+            for (int u = 0; u < kSlots; u++) {
+                const int chunk = lane + 32 * u;
+                if (chunk >= chunks) continue;
+                const uint4 v = t[i] < 0 ? make_uint4(0, 0, 0, 0) : read_values<F>(raw[i], u);
+                if constexpr (sizeof(T) == 2) {
+                    reinterpret_cast<uint4 *>(dst)[chunk] = v;
+                } else {
+                    const float2 f0 = bf16x2_to_f32(v.x), f1 = bf16x2_to_f32(v.y), f2 = bf16x2_to_f32(v.z),
+                                 f3 = bf16x2_to_f32(v.w);
+                    reinterpret_cast<float4 *>(dst)[2 * chunk] = make_float4(f0.x, f0.y, f1.x, f1.y);
+                    reinterpret_cast<float4 *>(dst)[2 * chunk + 1] = make_float4(f2.x, f2.y, f3.x, f3.y);
+                }
+            }
+            if (lane < dr / 2) {
+                const uint32_t v = t[i] < 0 ? 0u : pe[i];
+                if constexpr (sizeof(T) == 2)
+                    reinterpret_cast<uint32_t *>(dst + dc)[lane] = v;
+                else
+                    reinterpret_cast<float2 *>(dst + dc)[lane] = bf16x2_to_f32(v);
+            }
         }
     }
 }
 
-unsigned warp_grid(int64_t rows) {
-    const int64_t blocks = (rows + kWarps - 1) / kWarps, cap = (int64_t)num_sms() * 16;
-    return (unsigned)(blocks < cap ? blocks : cap);
+// `cap` blocks per SM at most (the kernels stride over the rest)
+unsigned warp_grid(int64_t rows, int cap) {
+    const int64_t blocks = (rows + kWarps - 1) / kWarps, most = (int64_t)num_sms() * cap;
+    return (unsigned)(blocks < most ? blocks : most);
 }
 
 template <typename T>
 void launch_prologue(dsa_dtype fmt, const PrologueArgs &a, cudaStream_t st) {
-    const unsigned grid = warp_grid(a.rows);
+    const int64_t blocks = (a.rows + 2 * kProWarps - 1) / (2 * kProWarps);
+    const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)num_sms() * kProBlocks);   // each warp strides on
     if (fmt == DSA_BF16)
-        latent_prologue_kernel<DSA_BF16, T><<<grid, 32 * kWarps, 0, st>>>(a);
+        latent_prologue_kernel<DSA_BF16, T><<<grid, 32 * kProWarps, 0, st>>>(a);
     else if (fmt == DSA_FP8_LATENT)
-        latent_prologue_kernel<DSA_FP8_LATENT, T><<<grid, 32 * kWarps, 0, st>>>(a);
+        latent_prologue_kernel<DSA_FP8_LATENT, T><<<grid, 32 * kProWarps, 0, st>>>(a);
     else
-        latent_prologue_kernel<DSA_Q4_LATENT, T><<<grid, 32 * kWarps, 0, st>>>(a);
+        latent_prologue_kernel<DSA_Q4_LATENT, T><<<grid, 32 * kProWarps, 0, st>>>(a);
+}
+
+template <int F, typename T>
+void launch_read_fmt(const uint8_t *cache, int64_t t_max, const int32_t *idx, int64_t start_pos, int64_t rows,
+                     int64_t n, int dc, int dr, T *out, cudaStream_t st) {
+    int *err = device_error_word();
+    // rows that leave every SM's warps one each are read one by one, more of
+    // them four at a time
+    if (rows <= (int64_t)num_sms() * 8 * kWarps)
+        latent_read_kernel<F, T, 1><<<warp_grid(rows, 8), 32 * kWarps, 0, st>>>(cache, t_max, idx, start_pos, rows, n, dc, dr, out, err);
+    else
+        latent_read_kernel<F, T, 4><<<warp_grid((rows + 3) / 4, 1 << 16), 32 * kWarps, 0, st>>>(cache, t_max, idx, start_pos, rows, n, dc, dr, out, err);
 }
 
 template <typename T>
 void launch_read(dsa_dtype fmt, const uint8_t *cache, int64_t t_max, const int32_t *idx, int64_t start_pos,
                  int64_t rows, int64_t n, int dc, int dr, T *out, cudaStream_t st) {
-    const unsigned grid = warp_grid(rows);
-    int *err = device_error_word();
     if (fmt == DSA_BF16)
-        latent_read_kernel<DSA_BF16, T><<<grid, 32 * kWarps, 0, st>>>(cache, t_max, idx, start_pos, rows, n, dc, dr, out, err);
+        launch_read_fmt<DSA_BF16>(cache, t_max, idx, start_pos, rows, n, dc, dr, out, st);
     else if (fmt == DSA_FP8_LATENT)
-        latent_read_kernel<DSA_FP8_LATENT, T><<<grid, 32 * kWarps, 0, st>>>(cache, t_max, idx, start_pos, rows, n, dc, dr, out, err);
+        launch_read_fmt<DSA_FP8_LATENT>(cache, t_max, idx, start_pos, rows, n, dc, dr, out, st);
     else
-        latent_read_kernel<DSA_Q4_LATENT, T><<<grid, 32 * kWarps, 0, st>>>(cache, t_max, idx, start_pos, rows, n, dc, dr, out, err);
+        launch_read_fmt<DSA_Q4_LATENT>(cache, t_max, idx, start_pos, rows, n, dc, dr, out, st);
 }
 
 }  // namespace
@@ -300,6 +563,7 @@ extern "C" dsa_status dsa_latent_read(const void *cache, dsa_dtype cache_dt, int
     if (!dsa::latent_shape_ok(dc, dr)) return DSA_ERR_UNSUPPORTED;
     if (!idx && start_pos + n > t_max) return DSA_ERR_INVALID_ARG;
     if (B == 0 || n == 0) return DSA_OK;
+    if (t_max == 0) return DSA_ERR_INVALID_ARG;            // no row to name
     if (!cache || !out || !dsa::aligned16(cache) || !dsa::aligned16(out) ||
         (reinterpret_cast<uintptr_t>(idx) & 3))
         return DSA_ERR_INVALID_ARG;
