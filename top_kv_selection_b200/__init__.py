@@ -113,8 +113,15 @@ def _ptr(t: torch.Tensor | None):
     return ctypes.c_void_p(t.data_ptr())
 
 
+# The current stream's handle without the Stream object that
+# torch.cuda.current_stream() builds (3 us a call, a quarter of a small call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
 
@@ -136,22 +143,48 @@ def _kv_dtype(kv_cache: torch.Tensor, q_mla: torch.Tensor, dc: int) -> int:
     return DSA_Q4_LATENT if kv_cache.shape[-1] == q4 else DSA_FP8_LATENT
 
 
-def _check_rows(cache: torch.Tensor, cache_dt: int, dc: int, dr: int) -> None:
-    """The cache [B, t_max, row] has rows of its format."""
+_ROW_BYTES = {}
+
+
+def _row_bytes(cache_dt: int, dc: int, dr: int) -> int:
+    key = (cache_dt, dc, dr)
+    if key not in _ROW_BYTES:
+        _ROW_BYTES[key] = int((_lib.dsa_latent_q4_row_bytes if cache_dt == DSA_Q4_LATENT
+                               else _lib.dsa_latent_row_bytes)(dc, dr))
+    return _ROW_BYTES[key]
+
+
+def _check_rows(cache: torch.Tensor, cache_dt: int, B: int, dc: int, dr: int) -> None:
+    """The cache [B, t_max, row] has B sequences of rows of its format."""
     if cache_dt == DSA_BF16:
         ok = cache.dtype == torch.bfloat16 and cache.shape[-1] == dc + dr
     else:
-        row = (_lib.dsa_latent_q4_row_bytes if cache_dt == DSA_Q4_LATENT
-               else _lib.dsa_latent_row_bytes)(dc, dr)
-        ok = cache.dtype == torch.uint8 and cache.shape[-1] == row
-    if cache.dim() != 3 or not ok:
-        raise ValueError(f"the cache [B, t_max, row] {tuple(cache.shape)} {cache.dtype} does not "
-                         f"have the rows of its format at dc = {dc}, dr = {dr}")
+        ok = cache.dtype == torch.uint8 and cache.shape[-1] == _row_bytes(cache_dt, dc, dr)
+    if not ok or cache.dim() != 3 or cache.shape[0] != B:
+        raise ValueError(f"the cache {tuple(cache.shape)} {cache.dtype} is not [{B}, t_max, row] with "
+                         f"the rows of its format at dc = {dc}, dr = {dr}")
 
 
 def _check_tensor(name: str, t: torch.Tensor | None, shape: tuple, dtype: torch.dtype) -> None:
-    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
-        raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype}, not {tuple(shape)} {dtype}")
+    if t is not None and (t.shape != shape or t.dtype != dtype):
+        raise ValueError(f"{name} is {tuple(t.shape)} {t.dtype}, not {shape} {dtype}")
+
+
+def _addr(*tensors: torch.Tensor | None) -> list:
+    """Device addresses of contiguous tensors on the current device (None for None)."""
+    dev = torch.cuda.current_device()
+    out = []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        if t.get_device() != dev:
+            raise ValueError(f"libdsa takes CUDA tensors on the current device only (cuda:{dev}), "
+                             f"got {t.device}")
+        if not t.is_contiguous():
+            raise ValueError("libdsa takes contiguous tensors only")
+        out.append(t.data_ptr())
+    return out
 
 
 def dsa_get_device_error(stream=None) -> int:
@@ -332,19 +365,17 @@ def dsa_latent_prologue(kv: torch.Tensor, norm_w: torch.Tensor | None, eps: floa
     start_pos to cache [B, t_max, row] in format cache_dt."""
     B, S, dqk = kv.shape
     dr = dqk - dc
-    if not kv.is_cuda:
-        raise ValueError("libdsa takes CUDA tensors only")
-    if dqk > 1 and kv.stride(-1) != 1:
+    if kv.stride(-1) != 1:
         raise ValueError("the last axis of kv must be contiguous")
-    _check_rows(cache, cache_dt, dc, dr)
-    if cache.shape[0] != B:
-        raise ValueError(f"kv has {B} sequences, the cache {cache.shape[0]}")
+    if kv.get_device() != torch.cuda.current_device():
+        raise ValueError(f"libdsa takes CUDA tensors on the current device only, got {kv.device}")
+    _check_rows(cache, cache_dt, B, dc, dr)
     _check_tensor("norm_w", norm_w, (dc,), torch.float32)
     _check_tensor("rope_cs", rope_cs, (S, dr // 2, 2), torch.float32)
+    p = _addr(norm_w, rope_cs, cache)
     _check("dsa_latent_prologue", _lib.dsa_latent_prologue(
-        ctypes.c_void_p(kv.data_ptr()), _dtype(kv), kv.stride(0), kv.stride(1), B, S, dc, dr,
-        _ptr(norm_w), eps, _ptr(rope_cs), 1 if interleaved else 0, start_pos, cache.shape[1],
-        _ptr(cache), cache_dt, _stream(stream)))
+        kv.data_ptr(), _dtype(kv), kv.stride(0), kv.stride(1), B, S, dc, dr, p[0], eps, p[1],
+        1 if interleaved else 0, start_pos, cache.shape[1], p[2], cache_dt, _stream(stream)))
 
 
 def dsa_latent_read(cache: torch.Tensor, cache_dt: int, start_pos: int, out: torch.Tensor,
@@ -352,24 +383,27 @@ def dsa_latent_read(cache: torch.Tensor, cache_dt: int, start_pos: int, out: tor
     """out [B,n,dc+dr] (bf16 or fp32) = the values of rows start_pos .. start_pos + n - 1 of
     cache [B, t_max, row], or of the rows idx [B,n] int32 (zeros for an index < 0)."""
     B, n, dqk = out.shape
-    _check_rows(cache, cache_dt, dc, dqk - dc)
-    if cache.shape[0] != B:
-        raise ValueError(f"out has {B} sequences, the cache {cache.shape[0]}")
+    _check_rows(cache, cache_dt, B, dc, dqk - dc)
     _check_tensor("idx", idx, (B, n), torch.int32)
+    p = _addr(cache, idx, out)
     _check("dsa_latent_read", _lib.dsa_latent_read(
-        _ptr(cache), cache_dt, cache.shape[1], _ptr(idx), start_pos, B, n, dc, dqk - dc, _ptr(out),
-        _dtype(out), _stream(stream)))
+        p[0], cache_dt, cache.shape[1], p[1], start_pos, B, n, dc, dqk - dc, p[2], _dtype(out),
+        _stream(stream)))
 
 
 def _check_attn(q: torch.Tensor, cache: torch.Tensor, cache_dt: int, sel: torch.Tensor, dc: int,
                 out: torch.Tensor, lse: torch.Tensor | None) -> None:
     B, S, Hq, dqk = q.shape
-    _check_rows(cache, cache_dt, dc, dqk - dc)
-    if q.dtype != torch.bfloat16 or cache.shape[0] != B:
-        raise ValueError("q must be bf16, the cache hold q's sequences")
+    if q.dtype != torch.bfloat16:
+        raise ValueError("q must be bf16")
+    _check_rows(cache, cache_dt, B, dc, dqk - dc)
     _check_tensor("the selection", sel, (B, S, sel.shape[-1]), torch.int32)
     _check_tensor("out", out, (B, S, Hq, dc), torch.bfloat16)
     _check_tensor("lse", lse, (B, S, Hq), torch.float32)
+
+
+def _bytes(workspace: torch.Tensor | None) -> int:
+    return workspace.numel() * workspace.element_size() if workspace is not None else 0
 
 
 def dsa_sparse_mla_attn_q4_workspace_size(B: int, S: int, Hq: int, dc: int, dr: int,
@@ -385,10 +419,10 @@ def dsa_sparse_mla_attn_q4(q: torch.Tensor, kv_q4: torch.Tensor, idx: torch.Tens
     out [B,S,Hq,dc] bf16, lse [B,S,Hq] fp32."""
     B, S, Hq, dqk = q.shape
     _check_attn(q, kv_q4, DSA_Q4_LATENT, idx, dc, out, lse)
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    p = _addr(q, kv_q4, idx, out, lse, workspace)
     _check("dsa_sparse_mla_attn_q4", _lib.dsa_sparse_mla_attn_q4(
-        _ptr(q), _ptr(kv_q4), kv_q4.shape[1], _ptr(idx), B, S, Hq, dc, dqk - dc, idx.shape[-1],
-        start_pos, sm_scale, _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)))
+        p[0], p[1], kv_q4.shape[1], p[2], B, S, Hq, dc, dqk - dc, idx.shape[-1], start_pos,
+        sm_scale, p[3], p[4], p[5], _bytes(workspace), _stream(stream)))
 
 
 def dsa_block_keys(k_cache: torch.Tensor, k_scale: torch.Tensor, start_pos: int, S: int,
@@ -403,9 +437,9 @@ def dsa_block_keys(k_cache: torch.Tensor, k_scale: torch.Tensor, start_pos: int,
     _check_tensor("k_scale", k_scale, (B, t_max), torch.float32)
     _check_tensor("blk_cache", blk_cache, (B, n_max, D), torch.uint8)
     _check_tensor("blk_scale", blk_scale, (B, n_max), torch.float32)
+    p = _addr(k_cache, k_scale, blk_cache, blk_scale)
     _check("dsa_block_keys", _lib.dsa_block_keys(
-        _ptr(k_cache), _ptr(k_scale), t_max, B, start_pos, S, D, block, _ptr(blk_cache),
-        _ptr(blk_scale), n_max, _stream(stream)))
+        p[0], p[1], t_max, B, start_pos, S, D, block, p[2], p[3], n_max, _stream(stream)))
 
 
 def dsa_block_mla_attn_workspace_size(B: int, S: int, Hq: int, dc: int, dr: int, kb: int,
@@ -422,11 +456,10 @@ def dsa_block_mla_attn(q: torch.Tensor, kv_cache: torch.Tensor, cache_dt: int, b
     query's own unfinished block is attended too."""
     B, S, Hq, dqk = q.shape
     _check_attn(q, kv_cache, cache_dt, blk, dc, out, lse)
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    p = _addr(q, kv_cache, blk, out, lse, workspace)
     _check("dsa_block_mla_attn", _lib.dsa_block_mla_attn(
-        _ptr(q), _ptr(kv_cache), cache_dt, kv_cache.shape[1], _ptr(blk), B, S, Hq, dc, dqk - dc,
-        blk.shape[-1], block, start_pos, sm_scale, _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes,
-        _stream(stream)))
+        p[0], p[1], cache_dt, kv_cache.shape[1], p[2], B, S, Hq, dc, dqk - dc, blk.shape[-1], block,
+        start_pos, sm_scale, p[3], p[4], p[5], _bytes(workspace), _stream(stream)))
 
 
 def dsa_decode_step_workspace_size(B: int, H: int, D: int, T: int, index_topk: int, Hq: int,
