@@ -74,7 +74,7 @@ def check(q, rows, sel, block, sp, sm, dc, out, lse):
                 continue
             c = rows[b][np.asarray(pos)]
             p = np.exp(sm * qd[b, s] @ c.T - rl[:, None])
-            dz = 2 * sm * d * 2.0 ** -24 * (np.abs(qd[b, s]) @ np.abs(c).T).max(-1, keepdims=True)
+            dz = 2 * abs(sm) * d * 2.0 ** -24 * (np.abs(qd[b, s]) @ np.abs(c).T).max(-1, keepdims=True)
             tol = (p @ np.abs(c[:, :dc])) * (2.0 ** -8 + 2 * dz + 2.0 ** -16) + np.abs(ro) * 2.0 ** -8
             err = np.abs(o[b, s] - ro)
             assert np.all(err <= tol), f"({b},{s}): {np.nanmax(err / np.maximum(tol, 1e-30)):.3g} x tolerance"
@@ -229,6 +229,28 @@ def test_growing_logits_move_the_running_maximum(dsa):
     check(q[:, :1], rows, idx[:, :1], 0, t_max - 300, 0.1, dc, out[:, :1], lse[:, :1])
     for s in sub.tolist():
         check(q[:, s:s + 1], rows, idx[:, s:s + 1], 0, t_max - 300 + s, 0.1, dc, out[:, s:s + 1], lse[:, s:s + 1])
+
+
+@pytest.mark.parametrize("shift", [-3000.0, -200.0, 200.0])
+def test_first_tiles_with_nothing_selected_and_logits_far_from_zero(dsa, shift):
+    """The first 128-slot tiles hold no valid slot; the logits that follow are far from zero, so
+    a reference of zero would lose them all (or overflow)."""
+    dc, dr, t_max, k = 512, 64, 600, 512
+    g = torch.Generator().manual_seed(5)
+    dirn = torch.randn(dc + dr, generator=g)
+    kv = torch.randn(1, t_max, dc + dr, generator=g) * 0.2 + dirn
+    raw = torch.zeros(1, t_max, 416, dtype=torch.uint8, device="cuda")
+    dsa.dsa_latent_prologue(kv.cuda(), None, 0.0, None, False, 0, raw, R.Q4, dc)
+    rows = R.decode_rows(raw.cpu().numpy(), R.Q4, dc, dr)
+    for S in (1, 200):                                   # one tile a CTA, and every tile in one CTA
+        q = (dirn + 0.05 * torch.randn(1, S, 64, dc + dr, generator=g)).to(torch.bfloat16)
+        sm = shift / float(dirn @ dirn)
+        idx = torch.full((1, S, k), -1, dtype=torch.int32)
+        idx[:, :, 300:] = torch.arange(k - 300, dtype=torch.int32)
+        out, lse = run_attn(dsa, q.cuda(), raw, R.Q4, idx.cuda(), 0, t_max - S, sm, dc)
+        for s in range(0, S, 50):
+            check(q[:, s:s + 1], rows, idx[:, s:s + 1], 0, t_max - S + s, sm, dc,
+                  out[:, s:s + 1], lse[:, s:s + 1])
 
 
 def test_no_lse_and_repeat_is_bitwise_equal(dsa):

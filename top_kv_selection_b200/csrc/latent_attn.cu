@@ -52,6 +52,9 @@ constexpr int kThreads = kWork + 32;
 constexpr int kMaxHeads = 64;                   // heads per CTA
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+// stands for a head's reference until it has one: every finite logit passes it
+// by more than the slack, and 2^(-inf - kUnseen) is 0
+constexpr float kUnseen = -1e30f;
 constexpr float kSlack = 8.f;                   // how far (log2) a logit may pass the reference
 
 struct AttnArgs {
@@ -74,8 +77,7 @@ struct AttnArgs {
 struct alignas(16) Control {
     float red[4][kMaxHeads];    // per TMEM lane quarter: maxima, later sums
     float ref[kMaxHeads];       // the heads' references (-inf: no logit seen)
-    float sub[kMaxHeads];       // the same, 0 instead of -inf: what is subtracted
-    float lim[kMaxHeads];       // reference + slack: a logit above it moves the reference
+    float sub[kMaxHeads];       // what is subtracted: the reference, or kUnseen
     float fac[kMaxHeads];       // rescaling of this tile; at the end 1 / sum
     uint64_t full[5];           // chunk pair m (4: the rotary chunk) is in shared memory
     uint64_t q_full, s_done, p_full, mma_fin;
@@ -244,7 +246,6 @@ template <int F, int NH>
 __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs a) {
     // heads per work thread (of 16 heads, the first two quarters take eight each)
     constexpr int kCols = NH == 16 ? 8 : NH / 4;
-    constexpr int kStep = 8;                               // logits a softmax thread holds at a time
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int nc = a.dc / 64, mt = a.dc / 128;             // latent chunks, dc tiles
@@ -260,10 +261,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
                            : NH * (mt + 1) <= 256 ? 256 : 512;
     if (warp == kWork / 32) {
         if (lane == 0) {
-            for (int i = 0; i < 5; i++) tc::mbar_init(&ctl.full[i], kWork);
+            // (a warp arrives once; copies in flight arrive for each thread)
+            for (int i = 0; i < 4; i++) tc::mbar_init(&ctl.full[i], F == DSA_BF16 ? kWork : kWork / 32);
+            tc::mbar_init(&ctl.full[4], kWork / 32);
             tc::mbar_init(&ctl.q_full, kWork);
             tc::mbar_init(&ctl.s_done, 1);
-            tc::mbar_init(&ctl.p_full, kWork);
+            tc::mbar_init(&ctl.p_full, 1);
             tc::mbar_init(&ctl.mma_fin, 1);
             for (int i = 0; i < 4; i++) tc::mbar_init(&ctl.o_done[i], 1);
             ctl.abort = 0;
@@ -276,8 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
     }
     if (threadIdx.x < NH) {
         ctl.ref[threadIdx.x] = -INFINITY;
-        ctl.sub[threadIdx.x] = 0.f;
-        ctl.lim[threadIdx.x] = -INFINITY;
+        ctl.sub[threadIdx.x] = kUnseen;
     }
     tc::tc_fence_before();
     __syncthreads();
@@ -360,7 +362,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
                     cp_async_arrive(&ctl.full[m]);
                 } else {
                     store_pair<F>(raw, m, tile, p8, j0, j1);
-                    tc::mbar_arrive(&ctl.full[m]);
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&ctl.full[m]);
                 }
             }
             st_shared_v4(pbase + j0 * 128 + ((p8 ^ (j0 & 7)) << 4), raw.rope0);
@@ -376,7 +379,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
                     ctl.valid[i & 1][kTile / 8 + warp] = (uint8_t)((y & 5) << 1 | (y >> 1 & 5));
                 }
             }
-            tc::mbar_arrive(&ctl.full[4]);
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&ctl.full[4]);
             t0 = __shfl_sync(0xffffffffu, town, 0, 8);
             t1 = __shfl_sync(0xffffffffu, town, 4, 8);
             load_rows<F>(raw, a, rbase, t0, t1, p8);       // (rows past the share's end are -1)
@@ -394,31 +398,46 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
             if (!tc::mbar_wait(&ctl.s_done, i & 1, a.err, abort)) ok = false;
             tc::tc_fence_after();
             const bool valid = ctl.valid[i & 1][key >> 2] >> (key & 3) & 1;
+            // weights against the standing references; whether a logit passes
+            // its reference by too much is known to all only behind them
+            float p[kCols];
             bool over = false;
-#pragma unroll
-            for (int x = 0; active && x < kCols; x += kStep) {
-                uint32_t v[kStep];
-                ld_cols(scol + x, v);
+            auto weights = [&]() {
+                uint32_t v[kCols];
+                ld_cols(scol, v);
                 tc::tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < kStep; e += 4) {
-                    const float4 r = *reinterpret_cast<const float4 *>(&ctl.lim[c * kCols + x + e]);
-                    over |= __uint_as_float(v[e]) * a.scale_log2 > r.x || __uint_as_float(v[e + 1]) * a.scale_log2 > r.y ||
-                            __uint_as_float(v[e + 2]) * a.scale_log2 > r.z || __uint_as_float(v[e + 3]) * a.scale_log2 > r.w;
+                for (int x = 0; x < kCols; x += 8) {
+                    const float4 s0 = *reinterpret_cast<const float4 *>(&ctl.sub[c * kCols + x]);
+                    const float4 s1 = *reinterpret_cast<const float4 *>(&ctl.sub[c * kCols + x + 4]);
+                    const float sub[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+                    uint32_t pk[4];
+#pragma unroll
+                    for (int e = 0; e < 8; e++) {
+                        const float z = fmaf(__uint_as_float(v[x + e]), a.scale_log2, -sub[e]);
+                        over |= z > kSlack;
+                        p[x + e] = valid ? ex2(z) : 0.f;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; e++) pk[e] = bf16x2_bits(__floats2bfloat162_rn(p[x + 2 * e], p[x + 2 * e + 1]));
+                    st_shared_v4(pbase + key * 128 + (((c * (kCols / 8) + x / 8) ^ (key & 7)) << 4),
+                                 make_uint4(pk[0], pk[1], pk[2], pk[3]));
                 }
-            }
-            if (tc::named_barrier_any(1, kWork, over && valid)) {
+            };
+            // (no reference stands before the first tile)
+            if (i > 0 && active) weights();
+            tc::tc_fence_before();
+            if (i == 0 || tc::named_barrier_any(1, kWork, over && valid)) {
                 // new references: the tile's maxima, per lane quarter and then
                 // over the four
-#pragma unroll
-                for (int x = 0; active && x < kCols; x += kStep) {
-                    uint32_t v[kStep];
-                    ld_cols(scol + x, v);
+                if (active) {
+                    uint32_t v[kCols];
+                    ld_cols(scol, v);
                     tc::tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < kStep; e++) {
+                    for (int e = 0; e < kCols; e++) {
                         const float m = warp_max_redux(valid ? __uint_as_float(v[e]) * a.scale_log2 : -INFINITY);
-                        if (lane == e) ctl.red[q4][c * kCols + x + e] = m;
+                        if (lane == e) ctl.red[q4][c * kCols + e] = m;
                     }
                 }
                 tc::named_barrier(1, kWork);
@@ -428,57 +447,42 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
                                                 fmaxf(ctl.red[2][t], ctl.red[3][t])), old);
                     ctl.fac[t] = old == m ? 1.f : ex2(old - m);
                     ctl.ref[t] = m;
-                    ctl.lim[t] = m + kSlack;
-                    ctl.sub[t] = m == -INFINITY ? 0.f : m;
+                    ctl.sub[t] = m == -INFINITY ? kUnseen : m;
                 }
                 tc::named_barrier(1, kWork);
-                if (i > 0 && active) {
-                    // (the value mix of the tile before is complete: this
-                    // tile's logits were issued after it)
+                if (active) {
+                    if (i > 0) {
+                        // (the value mix of the tile before is complete: this
+                        // tile's logits were issued after it)
 #pragma unroll
-                    for (int e = 0; e < kCols; e++) lsum[e] *= ctl.fac[c * kCols + e];
+                        for (int e = 0; e < kCols; e++) lsum[e] *= ctl.fac[c * kCols + e];
 #pragma unroll 1
-                    for (int m = 0; m < mt; m++) {
+                        for (int m = 0; m < mt; m++) {
 #pragma unroll 1
-                        for (int x = 0; x < kCols; x += 8) {
-                            const uint32_t col = scol + NH * (m + 1) + x;
-                            uint32_t v[8];
-                            tc::tmem_ld8(col, v);
-                            tc::tmem_wait_ld();
+                            for (int x = 0; x < kCols; x += 8) {
+                                const uint32_t col = scol + NH * (m + 1) + x;
+                                uint32_t v[8];
+                                tc::tmem_ld8(col, v);
+                                tc::tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 8; e++)
-                                v[e] = __float_as_uint(__uint_as_float(v[e]) * ctl.fac[c * kCols + x + e]);
-                            tc::tmem_st8(col, v);
+                                for (int e = 0; e < 8; e++)
+                                    v[e] = __float_as_uint(__uint_as_float(v[e]) * ctl.fac[c * kCols + x + e]);
+                                tc::tmem_st8(col, v);
+                            }
                         }
+                        tc::tmem_wait_st();
                     }
-                    tc::tmem_wait_st();
+                    weights();
                 }
+                tc::tc_fence_before();
+                tc::named_barrier(1, kWork);
             }
+            // every warp's weights are behind the barrier
+            if (t == 0) tc::mbar_arrive(&ctl.p_full);
+            if (active) {
 #pragma unroll
-            for (int x = 0; active && x < kCols; x += kStep) {
-                uint32_t v[kStep];
-                ld_cols(scol + x, v);
-                tc::tmem_wait_ld();
-#pragma unroll
-                for (int u = 0; u < kStep / 8; u++) {
-                    const float4 s0 = *reinterpret_cast<const float4 *>(&ctl.sub[c * kCols + x + 8 * u]);
-                    const float4 s1 = *reinterpret_cast<const float4 *>(&ctl.sub[c * kCols + x + 8 * u + 4]);
-                    const float sub[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-                    uint32_t pk[4];
-#pragma unroll
-                    for (int e = 0; e < 8; e += 2) {
-                        const float p0 = valid ? ex2(fmaf(__uint_as_float(v[8 * u + e]), a.scale_log2, -sub[e])) : 0.f;
-                        const float p1 = valid ? ex2(fmaf(__uint_as_float(v[8 * u + e + 1]), a.scale_log2, -sub[e + 1])) : 0.f;
-                        lsum[x + 8 * u + e] += p0;
-                        lsum[x + 8 * u + e + 1] += p1;
-                        pk[e / 2] = bf16x2_bits(__floats2bfloat162_rn(p0, p1));
-                    }
-                    st_shared_v4(pbase + key * 128 + (((c * (kCols / 8) + x / 8 + u) ^ (key & 7)) << 4),
-                                 make_uint4(pk[0], pk[1], pk[2], pk[3]));
-                }
+                for (int e = 0; e < kCols; e++) lsum[e] += p[e];
             }
-            tc::tc_fence_before();
-            tc::mbar_arrive(&ctl.p_full);
         }
         // the heads' sums, over the warp's slots and then over the lane quarters
 #pragma unroll
