@@ -38,7 +38,9 @@
 // Shared memory bounds the walk: a 128 x 64 x 16 MMA reads 6 KB in its 49
 // cycles, and the decoded tile is written beside it.
 // Splits of a row (when there are fewer rows than SMs) leave fp32 partials that
-// a second kernel merges.
+// a second kernel merges (fp16 ones with a power of two per 32 columns halved
+// the bytes, but the maxima they need cost more than the bytes: 24.9 against
+// 21.2 us at eight rows of 2048 slots).
 #include "latent_rows.cuh"
 #include "tc_ptx.cuh"
 
@@ -485,10 +487,25 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
             }
         }
         // the heads' sums, over the warp's slots and then over the lane quarters
+        // (lanes trade halves of their heads until each holds one head, or a
+        // part of one)
+        if (active) {
+            int hd = 0;
 #pragma unroll
-        for (int e = 0; active && e < kCols; e++) {
-            const float s = warp_sum(lsum[e]);
-            if (lane == e) ctl.red[q4][c * kCols + e] = s;
+            for (int m = 16, n = kCols / 2; m > 0; m >>= 1, n >>= 1) {
+                const bool up = lane & m;
+                if (n > 0) {
+                    hd += up ? n : 0;
+#pragma unroll
+                    for (int e = 0; e < n; e++) {
+                        const float give = up ? lsum[e] : lsum[e + n], keep = up ? lsum[e + n] : lsum[e];
+                        lsum[e] = keep + __shfl_xor_sync(0xffffffffu, give, m);
+                    }
+                } else {
+                    lsum[0] += __shfl_xor_sync(0xffffffffu, lsum[0], m);
+                }
+            }
+            if ((lane & (32 / kCols - 1)) == 0) ctl.red[q4][c * kCols + hd] = lsum[0];
         }
         tc::named_barrier(1, kWork);
         if (t < heads) {
