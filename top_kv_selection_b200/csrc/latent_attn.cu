@@ -135,10 +135,29 @@ __device__ __forceinline__ float ex2(float x) {
 // a softmax thread's columns
 __device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t (&v)[8]) { tc::tmem_ld8(taddr, v); }
 __device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t (&v)[16]) { tc::tmem_ld16(taddr, v); }
-__device__ __forceinline__ float warp_max_redux(float v) {
-    float r;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-    return r;
+// Reduces N values over the warp's lanes: lanes trade halves of their values
+// until each holds one, or a part of one, in v[0]; returns which one that is
+// (the lanes that differ in the bits below 32 / N only hold the same).  N
+// shuffles; a redux for each value measured slower.
+template <int N, typename Op>
+__device__ __forceinline__ int reduce_lanes(float (&v)[N], Op op) {
+    const int lane = threadIdx.x & 31;
+    int which = 0;
+#pragma unroll
+    for (int m = 16, n = N / 2; m > 0; m >>= 1, n >>= 1) {
+        const bool up = lane & m;
+        if (n > 0) {
+            which += up ? n : 0;
+#pragma unroll
+            for (int e = 0; e < n; e++) {
+                const float give = up ? v[e] : v[e + n], keep = up ? v[e + n] : v[e];
+                v[e] = op(keep, __shfl_xor_sync(0xffffffffu, give, m));
+            }
+        } else {
+            v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], m));
+        }
+    }
+    return which;
 }
 
 // The cache row of a selection slot of query row `row`, or -1.  Slot 0's block
@@ -437,10 +456,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
                     ld_cols(scol, v);
                     tc::tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < kCols; e++) {
-                        const float m = warp_max_redux(valid ? __uint_as_float(v[e]) * a.scale_log2 : -INFINITY);
-                        if (lane == e) ctl.red[q4][c * kCols + e] = m;
-                    }
+                    for (int e = 0; e < kCols; e++) p[e] = valid ? __uint_as_float(v[e]) * a.scale_log2 : -INFINITY;
+                    const int e = reduce_lanes(p, [](float x, float y) { return fmaxf(x, y); });
+                    if ((lane & (32 / kCols - 1)) == 0) ctl.red[q4][c * kCols + e] = p[0];
                 }
                 tc::named_barrier(1, kWork);
                 if (t < NH) {
@@ -487,25 +505,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
             }
         }
         // the heads' sums, over the warp's slots and then over the lane quarters
-        // (lanes trade halves of their heads until each holds one head, or a
-        // part of one)
         if (active) {
-            int hd = 0;
-#pragma unroll
-            for (int m = 16, n = kCols / 2; m > 0; m >>= 1, n >>= 1) {
-                const bool up = lane & m;
-                if (n > 0) {
-                    hd += up ? n : 0;
-#pragma unroll
-                    for (int e = 0; e < n; e++) {
-                        const float give = up ? lsum[e] : lsum[e + n], keep = up ? lsum[e + n] : lsum[e];
-                        lsum[e] = keep + __shfl_xor_sync(0xffffffffu, give, m);
-                    }
-                } else {
-                    lsum[0] += __shfl_xor_sync(0xffffffffu, lsum[0], m);
-                }
-            }
-            if ((lane & (32 / kCols - 1)) == 0) ctl.red[q4][c * kCols + hd] = lsum[0];
+            const int e = reduce_lanes(lsum, [](float x, float y) { return x + y; });
+            if ((lane & (32 / kCols - 1)) == 0) ctl.red[q4][c * kCols + e] = lsum[0];
         }
         tc::named_barrier(1, kWork);
         if (t < heads) {
