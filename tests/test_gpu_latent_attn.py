@@ -253,6 +253,27 @@ def test_first_tiles_with_nothing_selected_and_logits_far_from_zero(dsa, shift):
                   out[:, s:s + 1], lse[:, s:s + 1])
 
 
+@pytest.mark.parametrize("S", [1, 200])                 # split over CTAs, and one CTA a row
+def test_nan_stays_where_it_belongs(dsa, S):
+    """A NaN in one head's query makes that head NaN, in a selected row every head of that
+    query; a NaN logit among finite ones is not lost in the merge of the splits."""
+    t_max, k = 1200, 1000
+    q = make_q(1, S, 32, 576, 1)
+    cache, rows = make_cache(dsa, 1, t_max, R.BF16, 512, 64, seed=2)
+    blk = torch.arange(60, dtype=torch.int32).repeat(1, S, 1)
+    sp = t_max - S
+    q[0, 0, 5, 17] = float("nan")
+    out, lse = run_attn(dsa, q.cuda(), cache, R.BF16, blk.cuda(), 16, sp, 0.04, 512)
+    assert out[0, 0, 5].isnan().all() and lse[0, 0, 5].isnan()
+    keep = [h for h in range(32) if h != 5]
+    assert not out[0, 0, keep].isnan().any() and not lse[0, 0, keep].isnan().any()
+    check(q[:, -1:] if S > 1 else q[:, :, :5], rows, blk[:, -1:], 16, sp + S - 1, 0.04, 512,
+          out[:, -1:] if S > 1 else out[:, :, :5], lse[:, -1:] if S > 1 else lse[:, :, :5])
+    cache[0, 700, 3] = float("nan")                      # in one share only
+    out, lse = run_attn(dsa, make_q(1, S, 32, 576, 1).cuda(), cache, R.BF16, blk.cuda(), 16, sp, 0.04, 512)
+    assert out[..., 3].isnan().all() and lse.isnan().all()
+
+
 def test_no_lse_and_repeat_is_bitwise_equal(dsa):
     q = make_q(4, 1, 128, 576, 1).cuda()
     cache, _ = make_cache(dsa, 4, 3000, R.Q4, 512, 64, seed=2)

@@ -173,6 +173,32 @@ def test_read_records_rows_past_the_cache(dsa):
     assert dsa.dsa_get_device_error() == dsa.DSA_OK
 
 
+@pytest.mark.parametrize("S", [1, 3, 64])
+def test_append_rounds_from_the_exact_value(dsa, S):
+    """Normed rows whose quotients and scales lie close to a border between two codes: the
+    stored code is the one of the exact value wherever that is not itself within 2^-40 of the
+    border (many rows, so that every near border is met)."""
+    dc, dr, B = 512, 64, 4096 // S
+    kv = make_kv(B, S, dc, dr, torch.bfloat16, 12 + S, spread=False)
+    w = (1 + 0.3 * torch.randn(dc, generator=torch.Generator().manual_seed(1)))
+    a = torch.rand(S, dr // 2, generator=torch.Generator().manual_seed(2), dtype=torch.float64) * 6.28
+    cs = torch.stack((a.cos(), a.sin()), -1).float()
+    ref = R.prologue(kv.double().numpy(), w.double().numpy(), 1e-6, cs.double().numpy(), True, dc)
+    for fmt in (R.Q4, R.BF16):
+        cache = new_cache(B, S, fmt, dc, dr)
+        dsa.dsa_latent_prologue(kv.cuda(), w.cuda(), 1e-6, cs.cuda(), True, 0, cache, fmt, dc)
+        got = R.decode_rows(to_bytes(cache), fmt, dc, dr)
+        assert np.array_equal(got[..., dc:], R.bf16(ref[..., dc:].astype(np.float32)))
+        if fmt == R.BF16:
+            assert np.array_equal(got[..., :dc], R.bf16(ref[..., :dc].astype(np.float32)))
+            continue
+        n, s = R.q4_groups(ref[..., :dc])
+        step = np.repeat(s, 32, -1)
+        quot = ref[..., :dc] / step
+        near = np.abs(np.abs(quot - np.floor(quot)) - 0.5) < 2.0 ** -40
+        assert np.all((got[..., :dc] == R.bf16(n * step)) | near)
+
+
 def test_append_on_another_stream_and_in_a_graph(dsa):
     B, dc, dr = 4, 512, 64
     kv = make_kv(B, 1, dc, dr, torch.bfloat16, 3).cuda()

@@ -19,7 +19,10 @@
 // leaving TMEM, and few heads cost few columns.  (With the heads as M, 512
 // output columns fill TMEM and each tile's result has to leave it.)
 //
-// One CTA = (query row, group of up to 64 heads, share of the row's slots).
+// One CTA = (query row, group of up to 64 heads, share of the row's slots).  (One
+// that stays and takes row after row, the output written under the next row's
+// logits, needs more registers than there are: 1063 against 957 us at 1024
+// queries.)
 // Sixteen work warps and one that issues the MMAs.  Per tile, a work warp
 //   - decodes the tile's rows (eight threads a row, two rows a thread) to bf16
 //     in 64-column chunks, 128B-swizzled K-major tiles that serve as the logits'
@@ -358,7 +361,22 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
         cp_async_arrive(&ctl.q_full);
         RawRows<F> raw;
         int32_t t0 = __shfl_sync(0xffffffffu, town, 0, 8), t1 = __shfl_sync(0xffffffffu, town, 4, 8);
+        // which of a tile's slots count, by one bit each, for the softmax: known
+        // a tile ahead, so that the barriers between order it
+        auto note_valid = [&](int i) {
+            // the warp's rows 4 warp .. 4 warp + 3 and those 64 further on
+            // (which trade places in pairs)
+            const uint32_t x0 = __ballot_sync(0xffffffffu, t0 >= 0), x1 = __ballot_sync(0xffffffffu, t1 >= 0);
+            auto pack = [](uint32_t x) { return (x & 1) | (x >> 7 & 2) | (x >> 14 & 4) | (x >> 21 & 8); };
+            if (lane == 0) {
+                const uint32_t y = pack(x1);
+                ctl.valid[i & 1][warp] = (uint8_t)pack(x0);
+                ctl.valid[i & 1][kTile / 8 + warp] = (uint8_t)((y & 5) << 1 | (y >> 1 & 5));
+            }
+        };
+        note_valid(0);
         load_rows<F>(raw, a, rbase, t0, t1, p8);
+        tc::named_barrier(1, kWork);
         town = row_of(1, own);
         float lsum[kCols];
 #pragma unroll
@@ -389,21 +407,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
             }
             st_shared_v4(pbase + j0 * 128 + ((p8 ^ (j0 & 7)) << 4), raw.rope0);
             st_shared_v4(pbase + j1 * 128 + ((p8 ^ (j1 & 7)) << 4), raw.rope1);
-            {
-                // the warp's rows 4 warp .. 4 warp + 3 and those 64 further on
-                const uint32_t x0 = __ballot_sync(0xffffffffu, t0 >= 0), x1 = __ballot_sync(0xffffffffu, t1 >= 0);
-                // (those trade places in pairs)
-                auto pack = [](uint32_t x) { return (x & 1) | (x >> 7 & 2) | (x >> 14 & 4) | (x >> 21 & 8); };
-                if (lane == 0) {
-                    const uint32_t y = pack(x1);
-                    ctl.valid[i & 1][warp] = (uint8_t)pack(x0);
-                    ctl.valid[i & 1][kTile / 8 + warp] = (uint8_t)((y & 5) << 1 | (y >> 1 & 5));
-                }
-            }
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&ctl.full[4]);
             t0 = __shfl_sync(0xffffffffu, town, 0, 8);
             t1 = __shfl_sync(0xffffffffu, town, 4, 8);
+            note_valid(i + 1);
             load_rows<F>(raw, a, rbase, t0, t1, p8);       // (rows past the share's end are -1)
             town = row_of(i + 2, own);
             if (i == 0 && !one_tile) {
@@ -515,7 +523,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
             // (l is NaN where a logit is: it passes through)
             ctl.fac[t] = l == 0.f ? 0.f : 1.f / l;
             if (a.splits > 1)
-                a.part_ml[(int64_t)blockIdx.x * NH + t] = make_float2(l == 0.f ? -INFINITY : ctl.ref[t], l);
+                // (a NaN sum makes the reference NaN, so that the merge keeps it)
+                a.part_ml[(int64_t)blockIdx.x * NH + t] = make_float2(l == 0.f ? -INFINITY : l != l ? l : ctl.ref[t], l);
             else if (a.lse)
                 a.lse[row * a.Hq + h0 + t] = l == 0.f ? -INFINITY : (ctl.ref[t] + log2f(l)) * kLn2;
         }
@@ -809,7 +818,7 @@ dsa_status check_attn(const void *q, const void *kv, int64_t t_max, const int32_
     if ((int64_t)B * S * Hq == 0) return DSA_OK;
     if (start_pos + S > t_max || t_max > INT32_MAX) return DSA_ERR_INVALID_ARG;
     if ((int64_t)B * S * n_sel > INT32_MAX || (int64_t)B * S * Hq > INT32_MAX ||
-        (int64_t)(n_sel + 1) * (block ? block : 1) > INT32_MAX)
+        (int64_t)(n_sel + 1) * (block ? block : 1) > 1 << 30)
         return DSA_ERR_UNSUPPORTED;
     if (!q || !kv || !sel || !out) return DSA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(kv) || !aligned16(out) || (reinterpret_cast<uintptr_t>(sel) & 3) ||

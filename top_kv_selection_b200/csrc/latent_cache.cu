@@ -103,7 +103,8 @@ __device__ __forceinline__ void widen(const RawRow<float> &r, float2 (&x)[kVals 
     pe[1] = r.pe[1];
 }
 
-// max |a|, |b| that a NaN passes through: a group holding one gets a NaN scale
+// The larger of a and b, a NaN passing through: a 4-bit group that holds one gets
+// a NaN scale, so that what it stands for is NaN (an FP8 code has its own NaN)
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -272,12 +273,12 @@ __global__ void __launch_bounds__(32 * kProWarps, kProBlocks) latent_prologue_ke
             }
         } else {
             float amax = 0.f;
-#pragma unroll
-            for (int e = 0; e < kVals / 2; e++) amax = max_nan(amax, max_nan(fabsf(x[e].x), fabsf(x[e].y)));
             if constexpr (F == DSA_FP8_LATENT) {
+#pragma unroll
+                for (int e = 0; e < kVals / 2; e++) amax = fmaxf(amax, fmaxf(fabsf(x[e].x), fabsf(x[e].y)));
                 // a block of 128 is four lanes'
-                amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
                 const float sc = div_rn_by(fmaxf(amax * rms, 1e-4f), 448.0f, 1.0f / 448.0f), rs = __frcp_rn(sc);
                 const float2 rs2 = splat(rs), ns2 = splat(-sc);
                 uint32_t words[kVals / 4];
@@ -304,6 +305,8 @@ __global__ void __launch_bounds__(32 * kProWarps, kProBlocks) latent_prologue_ke
                 }
                 if (on && has_c && (l16 & 3) == 0) reinterpret_cast<float *>(dst + a.dc)[l16 >> 2] = sc;
             } else {
+#pragma unroll
+                for (int e = 0; e < kVals / 2; e++) amax = max_nan(amax, max_nan(fabsf(x[e].x), fabsf(x[e].y)));
                 const float st = div_rn_by(max_nan(amax * rms, 1e-4f), 7.0f, 1.0f / 7.0f);
                 const __nv_bfloat16 sb = __float2bfloat16_rn(st);
                 const float sc = __bfloat162float(sb), rs = __frcp_rn(sc);

@@ -74,21 +74,6 @@ __device__ __forceinline__ uint4 fp8_decode8(uint32_t w0, uint32_t w1, float sc)
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// Latent values [8 chunk, 8 chunk + 8) of a row, as four bf16 pairs.
-template <int F>
-__device__ __forceinline__ uint4 latent_chunk8(const uint8_t *row, int dc, int dr, int chunk) {
-    if constexpr (F == DSA_BF16) {
-        return reinterpret_cast<const uint4 *>(row)[chunk];
-    } else if constexpr (F == DSA_FP8_LATENT) {
-        const uint32_t *c = reinterpret_cast<const uint32_t *>(row) + 2 * chunk;
-        return fp8_decode8(c[0], c[1], *reinterpret_cast<const float *>(row + dc + 4 * (chunk >> 4)));
-    } else {
-        const __nv_bfloat16 s = *reinterpret_cast<const __nv_bfloat16 *>(
-            row + latent_q4_scales_at(dc, dr) + 2 * (chunk >> 2));
-        return q4_decode8(reinterpret_cast<const uint32_t *>(row)[chunk], __halves2bfloat162(s, s));
-    }
-}
-
 __device__ __forceinline__ float2 bf16x2_to_f32(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
