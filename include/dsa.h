@@ -334,9 +334,11 @@ int64_t dsa_latent_q4_row_bytes(int dc, int dr);
  * last dr:
  *   c' = c * (mean(c^2) + eps)^-1/2 * norm_w      (norm_w NULL: c' = c)
  *   p' = p rotated by rope_cs[s]                  (rope_cs NULL: p' = p)
- * in fp32, then one rounding into row start_pos + s of the cache: bf16, the FP8
- * row (dsa_latent_quant's rounding) or the 4-bit row.  interleaved != 0 pairs
- * elements (2j, 2j + 1) as (re, im), 0 pairs (j, j + dr/2).
+ * then one rounding into row start_pos + s of the cache: bf16, the FP8 row
+ * (dsa_latent_quant's rounding) or the 4-bit row.  bf16 and 4-bit rows hold the
+ * rounding of the exact value (fp32 where that leaves no doubt, else 64 bits),
+ * FP8 rows that of the fp32 one.  interleaved != 0 pairs elements (2j, 2j + 1) as
+ * (re, im), 0 pairs (j, j + dr/2).
  *
  *   kv       vector (b, s) at kv + b * batch_stride + s * token_stride (strides
  *            in elements of x_dtype, F32 or BF16; both multiples of 16 bytes,
@@ -369,7 +371,7 @@ dsa_status dsa_latent_read(const void *cache, dsa_dtype cache_dt, int64_t t_max,
  * cache kv_q4 [B, t_max, dsa_latent_q4_row_bytes(dc, dr)], 16-byte aligned.
  *   q    [B,S,Hq,dc+dr] bf16 (16-byte aligned), idx [B,S,k] int32 (-1 = empty)
  *   out  [B,S,Hq,dc] bf16 (16-byte aligned), lse [B,S,Hq] fp32 or NULL
- * 1 <= Hq <= 1024; shapes as dsa_latent_quant.  Each query row's selection is
+ * Hq up to 1024, k up to 2^30 - 1; shapes as dsa_latent_quant.  Each query row's selection is
  * masked as in dsa_sparse_mla_attn (-1 and indices > start_pos + s are skipped;
  * a row with nothing left gives out = 0, lse = -inf).
  * Workspace: dsa_sparse_mla_attn_q4_workspace_size bytes (16-byte aligned).
@@ -389,8 +391,9 @@ dsa_status dsa_sparse_mla_attn_q4(const void *q, const uint8_t *kv_q4, int64_t t
  *
  * dsa_block_keys: the keys of the blocks that the tokens start_pos ..
  * start_pos + S - 1 finish (block e is the tokens [e block, (e + 1) block)).  A
- * block's key is the mean of its tokens' decoded keys (code * scale) in fp32,
- * quantised as dsa_indexer_quant quantises a rotated vector.
+ * block's key is the mean of its tokens' decoded keys (code * scale), quantised
+ * as dsa_indexer_quant quantises a rotated vector; codes are those of the exact
+ * mean (taken again in 64 bits where fp32 leaves them in doubt).
  *   k_cache [B,t_max,D] e4m3, k_scale [B,t_max] fp32: the indexer's key cache,
  *           the new tokens' keys already appended
  *   blk_cache [B,n_max,D] e4m3, blk_scale [B,n_max] fp32: entry e is written for
@@ -411,6 +414,7 @@ dsa_status dsa_block_keys(const uint8_t *k_cache, const float *k_scale, int64_t 
  * dsa_sparse_mla_attn_q4.
  *   kv_cache [B,t_max,row] in format cache_dt (DSA_BF16, DSA_FP8_LATENT or
  *            DSA_Q4_LATENT), 16-byte aligned;  blk [B,S,kb] int32
+ * block from 1 to 2^20, (kb + 1) * block up to 2^30 (else DSA_ERR_UNSUPPORTED).
  */
 size_t dsa_block_mla_attn_workspace_size(int B, int S, int Hq, int dc, int dr, int kb, int block);
 dsa_status dsa_block_mla_attn(const void *q, const void *kv_cache, dsa_dtype cache_dt,

@@ -129,12 +129,18 @@ def test_block_attention_checks(dsa):
 def test_workspace_checks(dsa):
     L = dsa._lib
     need = L.dsa_sparse_mla_attn_q4_workspace_size(1, 1, 128, 512, 64, 2048)
-    if need:
-        assert attn(dsa, False, wsb=need - 1) == WORKSPACE
-        assert attn(dsa, False, ws=NULL) == WORKSPACE
-        assert attn(dsa, False, ws=ODD) == WORKSPACE
+    assert attn(dsa, False, wsb=need - 1) == WORKSPACE
+    assert attn(dsa, False, ws=NULL) == WORKSPACE
+    assert attn(dsa, False, ws=ODD) == WORKSPACE
+    assert attn(dsa, False, k=0x7FFFFFFF) == UNSUPPORTED
+    assert attn(dsa, True, k=0x7FFFFFFF, m=1) == UNSUPPORTED
     assert L.dsa_sparse_mla_attn_q4_workspace_size(1, 1, 128, 500, 64, 2048) == 0
     assert L.dsa_block_mla_attn_workspace_size(1, 1, 128, 512, 64, 32, 0) == 0
+    assert L.dsa_block_mla_attn_workspace_size(1, 1, 128, 512, 64, 1 << 20, 1 << 20) == 0
+    assert L.dsa_block_mla_attn_workspace_size(1, 1, 128, 512, 64, 0x7FFFFFFF, 1) == 0
+    # partials for the splits of few rows, none once every SM has a row
+    assert 0 < need <= 20 << 20
+    assert L.dsa_sparse_mla_attn_q4_workspace_size(1, 4096, 128, 512, 64, 2048) == 0
     assert L.dsa_sparse_mla_attn_q4_workspace_size(0, 1, 128, 512, 64, 2048) == 0
 
 

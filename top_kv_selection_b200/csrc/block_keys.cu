@@ -127,11 +127,12 @@ block_keys_kernel(const uint8_t *__restrict__ k_cache, const float *__restrict__
         }
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, m));
-        sc = __double2float_rn(fmax(top, (double)1e-4f) / 448.0);
+        const double exact = fmax(top, (double)1e-4f) / 448.0;
+        sc = __double2float_rn(exact);
         lo = 0;
 #pragma unroll
         for (int d = 0; d < kOwn; d += 2)
-            lo |= e4m3x2_rn_sat(__double2float_rn(x[d] / sc), __double2float_rn(x[d + 1] / sc)) << (8 * d);
+            lo |= e4m3x2_rn_sat(__double2float_rn(x[d] / exact), __double2float_rn(x[d + 1] / exact)) << (8 * d);
     }
     uint8_t *dst = blk_cache + (b * n_max + e) * D + own;
     if constexpr (kOwn == 4)

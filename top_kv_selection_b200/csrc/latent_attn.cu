@@ -818,7 +818,7 @@ dsa_status check_attn(const void *q, const void *kv, int64_t t_max, const int32_
     if ((int64_t)B * S * Hq == 0) return DSA_OK;
     if (start_pos + S > t_max || t_max > INT32_MAX) return DSA_ERR_INVALID_ARG;
     if ((int64_t)B * S * n_sel > INT32_MAX || (int64_t)B * S * Hq > INT32_MAX ||
-        (int64_t)(n_sel + 1) * (block ? block : 1) > 1 << 30)
+        ((int64_t)n_sel + 1) * (block ? block : 1) > 1 << 30)
         return DSA_ERR_UNSUPPORTED;
     if (!q || !kv || !sel || !out) return DSA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(kv) || !aligned16(out) || (reinterpret_cast<uintptr_t>(sel) & 3) ||
@@ -834,7 +834,7 @@ dsa_status check_attn(const void *q, const void *kv, int64_t t_max, const int32_
 }  // namespace dsa
 
 extern "C" size_t dsa_sparse_mla_attn_q4_workspace_size(int B, int S, int Hq, int dc, int dr, int k) {
-    if (B <= 0 || S <= 0 || Hq <= 0 || k <= 0 || !dsa::latent_shape_ok(dc, dr)) return 0;
+    if (B <= 0 || S <= 0 || Hq <= 0 || k <= 0 || k >= 1 << 30 || !dsa::latent_shape_ok(dc, dr)) return 0;
     return dsa::latent_attn_workspace_bytes(B, S, Hq, dc, dr, k, 0);
 }
 
@@ -853,6 +853,7 @@ extern "C" dsa_status dsa_sparse_mla_attn_q4(const void *q, const uint8_t *kv_q4
 
 extern "C" size_t dsa_block_mla_attn_workspace_size(int B, int S, int Hq, int dc, int dr, int kb, int block) {
     if (B <= 0 || S <= 0 || Hq <= 0 || kb <= 0 || block <= 0 || !dsa::latent_shape_ok(dc, dr)) return 0;
+    if (((int64_t)kb + 1) * block > 1 << 30) return 0;     // (the call refuses it)
     return dsa::latent_attn_workspace_bytes(B, S, Hq, dc, dr, kb, block);
 }
 
