@@ -9,9 +9,9 @@
 // A warp owns a block: one 16-byte load gives a lane 16 dims of a token, so
 // D / 16 lanes cover a token and a warp 512 / D tokens per load.  Each lane
 // sums its dims over its tokens in fp32 (packed pairs, up to sixteen tokens'
-// loads in flight: 138 MB of keys take 27.7 us, eight at a time 30.5); the lanes of a token group then trade halves until each holds the
+// loads in flight: 138 MB of keys take 29.7 us; eight at a time cost 3 more); the lanes of a token group then trade halves until each holds the
 // sums of D / 32 dims, in a fixed order.  Codes that the fp32 mean leaves in
-// doubt are taken from a mean in 64 bits (about one block in 250).  The keys'
+// doubt are taken from a mean in 64 bits (about one block in 30).  The keys'
 // bytes (D + 4 per token) bound it from below; the decoding of the codes, some
 // ten instructions a token and warp, comes close.
 #include <type_traits>
@@ -100,25 +100,35 @@ block_keys_kernel(const uint8_t *__restrict__ k_cache, const float *__restrict__
     amax = warp_max(amax);
     float sc = __fdiv_rn(fmaxf(amax, 1e-4f), 448.0f);
     const float rs = __frcp_rn(sc);
-    // a quotient is in doubt when its fp32 error (2^-20 covers the sums of
-    // blocks of any usual length) reaches over a border between two codes
+    // A quotient is in doubt when its fp32 error may reach over a border between
+    // two codes: 2^-21 of the vector's largest (448), since the sum's error goes
+    // by its terms and not by what they cancel to, and 2^-20 of itself.
+    constexpr float kAbs = 448.f * 0x1p-21f;
     uint32_t lo = 0, hi = 0;
 #pragma unroll
     for (int d = 0; d < kOwn; d += 2) {
         const float q0 = v[d] * rs, q1 = v[d + 1] * rs;
-        lo |= e4m3x2_rn_sat(fmaf(q0, -0x1p-20f, q0), fmaf(q1, -0x1p-20f, q1)) << (8 * d);
-        hi |= e4m3x2_rn_sat(fmaf(q0, 0x1p-20f, q0), fmaf(q1, 0x1p-20f, q1)) << (8 * d);
+        const float d0 = fmaf(fabsf(q0), 0x1p-20f, kAbs), d1 = fmaf(fabsf(q1), 0x1p-20f, kAbs);
+        lo |= e4m3x2_rn_sat(q0 - d0, q1 - d1) << (8 * d);
+        hi |= e4m3x2_rn_sat(q0 + d0, q1 + d1) << (8 * d);
     }
     if (__any_sync(0xffffffffu, lo != hi)) {
         double x[kOwn], top = 0.0;
 #pragma unroll
         for (int d = 0; d < kOwn; d++) x[d] = 0.0;
         const uint8_t *k0 = k_cache + t0 * D + own;
-#pragma unroll 4
+#pragma unroll 16
         for (int t = 0; t < block; t++) {
             const double s = (double)k_scale[t0 + t];
+            uint32_t w;
+            if constexpr (kOwn == 4)
+                w = *reinterpret_cast<const uint32_t *>(k0 + (int64_t)t * D);
+            else
+                w = *reinterpret_cast<const uint16_t *>(k0 + (int64_t)t * D);
+            float f[4];
+            e4m3x4_to_f32(w, f[0], f[1], f[2], f[3]);
 #pragma unroll
-            for (int d = 0; d < kOwn; d++) x[d] = fma((double)e4m3_to_f32(k0[(int64_t)t * D + d]), s, x[d]);
+            for (int d = 0; d < kOwn; d++) x[d] = fma((double)f[d], s, x[d]);
         }
 #pragma unroll
         for (int d = 0; d < kOwn; d++) {
