@@ -410,7 +410,7 @@ dsa_status dsa_block_keys(const uint8_t *k_cache, const float *k_scale, int64_t 
  * unfinished block, the tokens [(i + 1) / block * block, i].  A listed block
  * counts when it is finished, 0 <= e < (i + 1) / block; other entries (-1, the
  * unfinished block, a block ahead of the query) are skipped.  Listed blocks must
- * be distinct.  Formulas, shapes, outputs and empty rows as
+ * be distinct; kb may be 0 (blk NULL): the unfinished block alone.  Formulas, shapes, outputs and empty rows as
  * dsa_sparse_mla_attn_q4.
  *   kv_cache [B,t_max,row] in format cache_dt (DSA_BF16, DSA_FP8_LATENT or
  *            DSA_Q4_LATENT), 16-byte aligned;  blk [B,S,kb] int32

@@ -108,7 +108,7 @@ def attn(dsa, blocks, **kw):
 @pytest.mark.parametrize("blocks", [False, True])
 @pytest.mark.parametrize("kw,status", [
     (dict(dc=500), UNSUPPORTED), (dict(dr=72), UNSUPPORTED), (dict(Hq=1025), UNSUPPORTED),
-    (dict(sp=4096), INVALID), (dict(sp=-1), INVALID), (dict(k=0), INVALID), (dict(B=-1), INVALID),
+    (dict(sp=4096), INVALID), (dict(sp=-1), INVALID), (dict(k=-1), INVALID), (dict(B=-1), INVALID),
     (dict(q=ODD), INVALID), (dict(kv=ODD), INVALID), (dict(out=ODD), INVALID), (dict(q=NULL), INVALID),
     (dict(sel=NULL), INVALID), (dict(out=NULL), INVALID), (dict(lse=ctypes.c_void_p((1 << 20) + 2)), INVALID),
     (dict(t_max=1 << 32), INVALID),
@@ -120,6 +120,9 @@ def test_attention_checks(dsa, blocks, kw, status):
 
 
 def test_block_attention_checks(dsa):
+    assert attn(dsa, False, k=0) == INVALID           # a list of positions is not empty
+    assert attn(dsa, True, k=1, sel=NULL) == INVALID
+    assert attn(dsa, True, k=0, sel=NULL, B=0) == OK
     assert attn(dsa, True, m=0) == INVALID
     assert attn(dsa, True, fmt=F32) == INVALID
     assert attn(dsa, True, k=1 << 20, m=1 << 20) == UNSUPPORTED

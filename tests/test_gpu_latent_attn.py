@@ -158,6 +158,15 @@ def test_block_lists_skip_unfinished_and_future_blocks(dsa, fmt):
     check(q, rows, blk, block, sp, 0.04, dc, out, lse)
 
 
+def test_no_finished_block_to_list(dsa):
+    """The first tokens of a sequence: no block is finished, the list has no columns."""
+    q = make_q(2, 5, 16, 576, 5)
+    cache, rows = make_cache(dsa, 2, 40, R.Q4, 512, 64, seed=6)
+    blk = torch.empty(2, 5, 0, dtype=torch.int32)
+    out, lse = run_attn(dsa, q.cuda(), cache, R.Q4, blk.cuda(), 64, 3, 0.04, 512)
+    check(q, rows, blk, 64, 3, 0.04, 512, out, lse)
+
+
 def test_empty_rows(dsa):
     B, S, Hq, dc, dr, t_max, k = 3, 2, 128, 512, 64, 300, 300
     q = make_q(B, S, Hq, dc + dr, 1)

@@ -812,7 +812,8 @@ dsa_status check_attn(const void *q, const void *kv, int64_t t_max, const int32_
                       int B, int S, int Hq, int dc, int dr, int64_t start_pos, const void *out, const float *lse,
                       const void *ws, size_t ws_bytes, bool *run) {
     *run = false;
-    if (B < 0 || S < 0 || Hq < 0 || n_sel < 1 || start_pos < 0) return DSA_ERR_INVALID_ARG;
+    // (without a finished block there is none to list: the unfinished one is attended)
+    if (B < 0 || S < 0 || Hq < 0 || n_sel < (block ? 0 : 1) || start_pos < 0) return DSA_ERR_INVALID_ARG;
     if (!latent_shape_ok(dc, dr)) return DSA_ERR_UNSUPPORTED;
     if (Hq > 1024 || block > 1 << 20) return DSA_ERR_UNSUPPORTED;
     if ((int64_t)B * S * Hq == 0) return DSA_OK;
@@ -820,7 +821,7 @@ dsa_status check_attn(const void *q, const void *kv, int64_t t_max, const int32_
     if ((int64_t)B * S * n_sel > INT32_MAX || (int64_t)B * S * Hq > INT32_MAX ||
         ((int64_t)n_sel + 1) * (block ? block : 1) > 1 << 30)
         return DSA_ERR_UNSUPPORTED;
-    if (!q || !kv || !sel || !out) return DSA_ERR_INVALID_ARG;
+    if (!q || !kv || (!sel && n_sel > 0) || !out) return DSA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(kv) || !aligned16(out) || (reinterpret_cast<uintptr_t>(sel) & 3) ||
         (reinterpret_cast<uintptr_t>(lse) & 3))
         return DSA_ERR_INVALID_ARG;
@@ -852,7 +853,7 @@ extern "C" dsa_status dsa_sparse_mla_attn_q4(const void *q, const uint8_t *kv_q4
 }
 
 extern "C" size_t dsa_block_mla_attn_workspace_size(int B, int S, int Hq, int dc, int dr, int kb, int block) {
-    if (B <= 0 || S <= 0 || Hq <= 0 || kb <= 0 || block <= 0 || !dsa::latent_shape_ok(dc, dr)) return 0;
+    if (B <= 0 || S <= 0 || Hq <= 0 || kb < 0 || block <= 0 || !dsa::latent_shape_ok(dc, dr)) return 0;
     if (((int64_t)kb + 1) * block > 1 << 30) return 0;     // (the call refuses it)
     return dsa::latent_attn_workspace_bytes(B, S, Hq, dc, dr, kb, block);
 }
