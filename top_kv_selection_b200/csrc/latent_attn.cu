@@ -278,7 +278,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
     volatile int *abort = &ctl.abort;
     const uint32_t tile = tc::smem_u32(sm), qbase = tc::smem_u32(qs);
     const uint32_t pbase = tile + nc * kRegion;            // P takes the rotary chunk's place
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (read through a shuffle, so that it is known to be the same in a warp)
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     // TMEM: the logits, then the output tiles
     const uint32_t ncols = NH * (mt + 1) <= 32 ? 32 : NH * (mt + 1) <= 64 ? 64 : NH * (mt + 1) <= 128 ? 128
@@ -308,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    const uint32_t tmem = ctl.tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, ctl.tmem, 0);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // every global read comes after this (a no-op without a programmatic launch)
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -415,14 +416,15 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
             load_rows<F>(raw, a, rbase, t0, t1, p8);       // (rows past the share's end are -1)
             town = row_of(i + 2, own);
             if (i == 0 && !one_tile) {
-                int last = -1;
+                int mine = -1;
 #pragma unroll 4
                 for (int s = lo + t; s < hi; s += kWork)
-                    if (slot_row(a, list, s, limit, done) >= 0) last = s;
-                last = __reduce_max_sync(0xffffffffu, last);
-                if (lane == 0 && last >= 0) atomicMax(&ctl.last, last);
+                    if (slot_row(a, list, s, limit, done) >= 0) mine = s;
+                mine = __reduce_max_sync(0xffffffffu, mine);
+                if (lane == 0 && mine >= 0) atomicMax(&ctl.last, mine);
                 tc::named_barrier(2, kThreads);
-                tiles = ctl.last < lo ? 1 : (ctl.last - lo) / kTile + 1;
+                const int last = __shfl_sync(0xffffffffu, ctl.last, 0);
+                tiles = last < lo ? 1 : (last - lo) / kTile + 1;
             }
             if (!tc::mbar_wait(&ctl.s_done, i & 1, a.err, abort)) ok = false;
             tc::tc_fence_after();
@@ -577,7 +579,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
                 if (i == 0 && !one_tile) {
                     tc::named_barrier(2, kThreads);
                     counted = true;
-                    tiles = ctl.last < lo ? 1 : (ctl.last - lo) / kTile + 1;
+                    const int last = __shfl_sync(0xffffffffu, ctl.last, 0);
+                    tiles = last < lo ? 1 : (last - lo) / kTile + 1;
                 }
                 if (!(ok = tc::mbar_wait(&ctl.p_full, ph, a.err, abort))) break;
                 tc::fence_proxy_async_smem();
