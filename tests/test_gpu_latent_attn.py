@@ -167,6 +167,55 @@ def test_no_finished_block_to_list(dsa):
     check(q, rows, blk, 64, 3, 0.04, 512, out, lse)
 
 
+def test_offsets_beyond_32_bits(dsa):
+    """A 5 GB cache: rows, blocks and keys whose byte offsets pass 2^32, written, read and
+    attended; the rows between are left alone."""
+    B, dc, dr, t_max, S = 2, 512, 64, 6_000_000, 3
+    cache = torch.empty(B, t_max, 416, dtype=torch.uint8, device="cuda")
+    g = torch.Generator().manual_seed(3)
+    near = list(range(40)) + list(range(t_max - 200, t_max))
+    kv = torch.randn(B, len(near), dc + dr, generator=g).to(torch.bfloat16).cuda()
+    dsa.dsa_latent_prologue(kv[:, :40], None, 0.0, None, False, 0, cache, R.Q4, dc)
+    dsa.dsa_latent_prologue(kv[:, 40:], None, 0.0, None, False, t_max - 200, cache, R.Q4, dc)
+    rows = R.decode_rows(cache[:, near].cpu().numpy(), R.Q4, dc, dr)
+    n, s = R.q4_groups(kv[..., :dc].double().cpu().numpy())
+    assert np.array_equal(rows[..., :dc], R.bf16(n * np.repeat(s, 32, -1)))
+    out = torch.empty(B, 200, dc + dr, device="cuda")
+    dsa.dsa_latent_read(cache, R.Q4, t_max - 200, out, dc)
+    assert np.array_equal(out.double().cpu().numpy(), rows[:, 40:])
+    # positions: the last ones and the first ones, a sequence's rows renumbered for the check
+    q = make_q(B, S, 32, dc + dr, 4)
+    idx = torch.tensor([t_max - 1, t_max - 2, t_max - 3, 5, -1, t_max - 150, 39], dtype=torch.int32).repeat(B, S, 1)
+    sp = t_max - S
+    o, lse = run_attn(dsa, q.cuda(), cache, R.Q4, idx.cuda(), 0, sp, 0.04, dc)
+    place = {t: i for i, t in enumerate(near)}
+    local = torch.tensor([[[place[t] if 0 <= t <= sp + s else -1 for t in idx[b, s].tolist()] for s in range(S)]
+                          for b in range(B)], dtype=torch.int32)
+    check(q, rows, local, 0, 10 ** 6, 0.04, dc, o, lse)
+    # blocks of 16: the last finished one and the second, and the unfinished one
+    blk = torch.tensor([(t_max - S) // 16 - 1, 1], dtype=torch.int32).repeat(B, S, 1)
+    o, lse = run_attn(dsa, q.cuda(), cache, R.Q4, blk.cuda(), 16, sp, 0.04, dc)
+    local = torch.full((B, S, 64), -1, dtype=torch.int32)
+    for b in range(B):
+        for s in range(S):
+            pos = R.block_positions(blk[b, s].tolist(), 16, sp + s)
+            local[b, s, :len(pos)] = torch.tensor([place[t] for t in pos], dtype=torch.int32)
+    check(q, rows, local, 0, 10 ** 6, 0.04, dc, o, lse)
+    del cache
+    # block keys at the end of a 4.4 GB key cache
+    T, D, m = 17_200_000, 128, 64
+    kc = torch.zeros(2, T, D, dtype=torch.uint8, device="cuda")
+    ks = torch.zeros(2, T, device="cuda")
+    kc[:, -128:] = torch.randint(0, 120, (2, 128, D), generator=g, dtype=torch.uint8).cuda()
+    ks[:, -128:] = 0.01
+    bc, bs = torch.zeros(2, T // m, D, dtype=torch.uint8, device="cuda"), torch.zeros(2, T // m, device="cuda")
+    dsa.dsa_block_keys(kc, ks, T - 128, 128, m, bc, bs)
+    want = np.stack([R.block_keys(kc[b, -128:].cpu().numpy(), ks[b, -128:].cpu().numpy(), m, D) for b in range(2)])
+    got = R.E4M3[bc[:, -2:].cpu().numpy()] * bs[:, -2:, None].double().cpu().numpy()
+    assert np.all(np.abs(got - want) <= np.abs(want) * 2.0 ** -4 + np.abs(want).max(-1, keepdims=True) * 2.0 ** -14)
+    assert not bs[:, :-2].any()
+
+
 def test_empty_rows(dsa):
     B, S, Hq, dc, dr, t_max, k = 3, 2, 128, 512, 64, 300, 300
     q = make_q(B, S, Hq, dc + dr, 1)
