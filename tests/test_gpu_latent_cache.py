@@ -199,6 +199,40 @@ def test_append_rounds_from_the_exact_value(dsa, S):
         assert np.all((got[..., :dc] == R.bf16(n * step)) | near)
 
 
+@pytest.mark.parametrize("fmt", [R.BF16, R.Q4])
+def test_append_of_extreme_and_nan_rows(dsa, fmt):
+    """Rows whose squares leave fp32's range (with and without eps) keep the exact norm; a NaN
+    makes its row NaN under a norm, its 4-bit group (or itself, in bf16) without one, and no
+    other row or group."""
+    dc, dr = 256, 16
+    kv = make_kv(4, 2, dc, dr, torch.float32, 5, spread=False)
+    kv[0] *= 1e25
+    kv[1] *= 1e-25
+    kv[2, 0, 40] = float("nan")
+    w = torch.ones(dc).cuda()
+    for eps in (0.0, 1e-6):
+        cache = new_cache(4, 2, fmt, dc, dr)
+        dsa.dsa_latent_prologue(kv.cuda(), w, eps, None, False, 0, cache, fmt, dc)
+        got = R.decode_rows(to_bytes(cache), fmt, dc, dr)[..., :dc]
+        ref = R.prologue(kv.double().numpy(), np.ones(dc), eps, None, False, dc)[..., :dc]
+        assert np.isnan(got[2, 0]).all()
+        keep = np.ones((4, 2), bool)
+        keep[2, 0] = False
+        if fmt == R.BF16:
+            want = R.bf16(ref.astype(np.float32))[keep]
+        else:
+            n, s = R.q4_groups(ref[keep])
+            want = R.bf16(n * np.repeat(s, 32, -1))
+        assert np.array_equal(got[keep], want)
+    cache = new_cache(4, 2, fmt, dc, dr)
+    dsa.dsa_latent_prologue(kv.cuda(), None, 0.0, None, False, 0, cache, fmt, dc)
+    got = R.decode_rows(to_bytes(cache), fmt, dc, dr)[..., :dc]
+    group = slice(32, 64) if fmt == R.Q4 else slice(40, 41)
+    assert np.isnan(got[2, 0, group]).all()
+    got[2, 0, group] = 0
+    assert np.isfinite(got).all()
+
+
 def test_append_on_another_stream_and_in_a_graph(dsa):
     B, dc, dr = 4, 512, 64
     kv = make_kv(B, 1, dc, dr, torch.bfloat16, 3).cuda()

@@ -151,9 +151,11 @@ __device__ __noinline__ void exact_row(const T *src, uint8_t *dst, const float *
             double amax = fabs(y);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) amax = fmax(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            const __nv_bfloat16 sb = __float2bfloat16_rn(__double2float_rn(fmax(amax, (double)1e-4f) / 7.0));
-            const int v = d & 7;
-            uint32_t code = (uint32_t)(8 + __double2int_rn(y / (double)__bfloat162float(sb))) << (4 * (v / 2 + 4 * (v & 1)));
+            float sf = __double2float_rn(fmax(amax, (double)1e-4f) / 7.0);
+            if (__any_sync(0xffffffffu, y != y)) sf = __int_as_float(0x7FC00000);   // a NaN makes the group NaN
+            const __nv_bfloat16 sb = __float2bfloat16_rn(sf);
+            const int v = d & 7, n = max(-7, min(7, __double2int_rn(y / (double)__bfloat162float(sb))));
+            uint32_t code = (uint32_t)(8 + n) << (4 * (v / 2 + 4 * (v & 1)));
 #pragma unroll
             for (int o = 1; o < 8; o <<= 1) code |= __shfl_xor_sync(0xffffffffu, code, o);
             if (v == 0) reinterpret_cast<uint32_t *>(dst)[d >> 3] = code;
@@ -236,6 +238,7 @@ __global__ void __launch_bounds__(32 * kProWarps, kProBlocks) latent_prologue_ke
         if (r + step < a.rows) fetch(at.b, at.s);
 
         float rms = 1.f;
+        bool doubt = false;
         if (norm) {
             float2 s0 = make_float2(0.f, 0.f), s1 = s0;
 #pragma unroll
@@ -249,6 +252,7 @@ __global__ void __launch_bounds__(32 * kProWarps, kProBlocks) latent_prologue_ke
             const float v = fmaf(ss, inv_dc, a.eps);
             rms = rsqrtf(v);
             rms = fmaf(rms * 0.5f, fmaf(-v * rms, rms, 1.f), rms);      // a Newton step: within a rounding or two
+            doubt = !(v > 0x1p-80f && v < 0x1p80f);        // squares that fp32 cannot hold
 #pragma unroll
             for (int e = 0; e < kVals / 4; e++) {
                 const float4 wv = w_sm[l16 * (kPitch / 4) + e];
@@ -257,7 +261,6 @@ __global__ void __launch_bounds__(32 * kProWarps, kProBlocks) latent_prologue_ke
                 x[2 * e + 1] = __fmul2_rn(x[2 * e + 1], make_float2(wv.z, wv.w));
             }
         }
-        bool doubt = false;
         if constexpr (F == DSA_BF16) {
 #pragma unroll
             for (int i = 0; i < 4; i++) {
@@ -323,7 +326,7 @@ __global__ void __launch_bounds__(32 * kProWarps, kProBlocks) latent_prologue_ke
                         const float2 d = __ffma2_rn(q, splat(-1.f), n);
                         far = fmaxf(far, fmaxf(fabsf(d.x), fabsf(d.y)));
                     }
-                    doubt = far > 0.5f - 0x1p-19f || ((__float_as_uint(st) + 0x8002u) & 0xFFFFu) < 4u;
+                    doubt |= far > 0.5f - 0x1p-19f || ((__float_as_uint(st) + 0x8002u) & 0xFFFFu) < 4u;
                 } else {
                     const float2 rs2 = splat(rs), ns2 = splat(-sc);
 #pragma unroll
