@@ -233,6 +233,32 @@ def test_append_of_extreme_and_nan_rows(dsa, fmt):
     assert np.isfinite(got).all()
 
 
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+@pytest.mark.parametrize("dc,dr", [(512, 64), (384, 40)])
+def test_fp8_append_of_extreme_rows(dsa, dc, dr, eps):
+    """Rows whose squares leave fp32's range, beside an ordinary one.  A code is off by half a
+    step (2^-4, or 2^-10 scales below the normal codes), the decoded bf16 by 2^-8, the fp32
+    chain with its scale by 2^-18 and a few roundings, 2^-17 together."""
+    kv = make_kv(3, 4, dc, dr, torch.float32, 6, spread=False)
+    for i, f in enumerate((1e25, 1e-25, 1e-18, 1.0, 5e37, 1e-30)):
+        kv[i // 4, i % 4] *= f
+    kv[2, 0, 7] = float("nan")
+    kv[2, 1, 9] = float("inf")
+    w = 1 + 0.2 * torch.randn(dc, generator=torch.Generator().manual_seed(8))
+    cache = new_cache(3, 4, R.FP8, dc, dr)
+    dsa.dsa_latent_prologue(kv.cuda(), w.cuda(), eps, None, False, 0, cache, R.FP8, dc)
+    got = R.decode_rows(to_bytes(cache), R.FP8, dc, dr)[..., :dc]
+    assert np.isnan(got[2, 0]).all()
+    assert np.isnan(got[2, 1, 9]) and not np.delete(got[2, 1], 9).any()
+    kv[2, :2] = 1
+    got[2, :2] = 0
+    ref = R.prologue(kv.double().numpy(), w.double().numpy(), eps, None, False, dc)[..., :dc]
+    ref[2, :2] = 0
+    scale = np.maximum(np.abs(ref).reshape(3, 4, -1, 128).max(-1), 1e-4) / 448
+    tol = np.abs(ref) * (2.0 ** -4 + 2.0 ** -8 + 2.0 ** -12 + 2.0 ** -17)
+    assert np.all(np.abs(got - ref) <= tol + np.repeat(scale, 128, -1) * 2.0 ** -10 * (1 + 2.0 ** -7))
+
+
 def test_append_on_another_stream_and_in_a_graph(dsa):
     B, dc, dr = 4, 512, 64
     kv = make_kv(B, 1, dc, dr, torch.bfloat16, 3).cuda()

@@ -240,19 +240,32 @@ __global__ void __launch_bounds__(32 * kProWarps, kProBlocks) latent_prologue_ke
         float rms = 1.f;
         bool doubt = false;
         if (norm) {
-            float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+            const auto mean_square = [&](float eps) {      // of the half warp's row, plus eps
+                float2 s0 = make_float2(0.f, 0.f), s1 = s0;
 #pragma unroll
-            for (int e = 0; e < kVals / 2; e += 2) {
-                s0 = __ffma2_rn(x[e], x[e], s0);
-                s1 = __ffma2_rn(x[e + 1], x[e + 1], s1);
-            }
-            float ss = (s0.x + s0.y) + (s1.x + s1.y);
+                for (int e = 0; e < kVals / 2; e += 2) {
+                    s0 = __ffma2_rn(x[e], x[e], s0);
+                    s1 = __ffma2_rn(x[e + 1], x[e + 1], s1);
+                }
+                float ss = (s0.x + s0.y) + (s1.x + s1.y);
 #pragma unroll
-            for (int m = 8; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-            const float v = fmaf(ss, inv_dc, a.eps);
-            rms = rsqrtf(v);
-            rms = fmaf(rms * 0.5f, fmaf(-v * rms, rms, 1.f), rms);      // a Newton step: within a rounding or two
+                for (int m = 8; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+                return fmaf(ss, inv_dc, eps);
+            };
+            float v = mean_square(a.eps);
             doubt = !(v > 0x1p-80f && v < 0x1p80f);        // squares that fp32 cannot hold
+            if constexpr (F == DSA_FP8_LATENT) {
+                // such a row is taken times a power of two, which the norm takes
+                // out again (the other formats round it from 64-bit sums below)
+                if (__any_sync(0xffffffffu, doubt)) {
+                    const float k = !doubt ? 1.f : v < 1.f ? 0x1p90f : 0x1p-80f;
+#pragma unroll
+                    for (int e = 0; e < kVals / 2; e++) x[e] = __fmul2_rn(x[e], splat(k));
+                    v = mean_square(a.eps * k * k);
+                }
+            }
+            rms = rsqrtf(v);
+            if (rms != 0.f) rms = fmaf(rms * 0.5f, fmaf(-v * rms, rms, 1.f), rms);      // a Newton step: within a rounding or two
 #pragma unroll
             for (int e = 0; e < kVals / 4; e++) {
                 const float4 wv = w_sm[l16 * (kPitch / 4) + e];
