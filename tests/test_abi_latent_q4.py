@@ -159,3 +159,22 @@ def test_decode_step_takes_the_4_bit_cache(dsa):
     assert call(dc=96) == UNSUPPORTED                 # a bf16 shape, not a 4-bit one
     assert call(Hq=1025) == UNSUPPORTED
     assert call(ws_bytes=need - 1) == WORKSPACE
+
+
+@pytest.mark.parametrize("sp", [(1 << 63) - 1, (1 << 63) - 4])
+def test_a_position_near_the_end_of_64_bits_is_refused(dsa, sp):
+    """Its sum with the number of tokens does not fit 64 bits."""
+    L = dsa._lib
+    assert prologue(L, sp=sp) == INVALID
+    assert read(L, sp=sp) == INVALID
+    assert keys(L, sp=sp) == INVALID
+    for blocks in (False, True):
+        assert attn(dsa, blocks, sp=sp, S=8) == INVALID
+
+
+def test_row_counts_past_64_bits_are_refused(dsa):
+    L = dsa._lib
+    for blocks in (False, True):          # B * S * Hq = 2^64
+        assert attn(dsa, blocks, B=1 << 30, S=1 << 30, Hq=16, sp=0, t_max=(1 << 31) - 1, k=16) == UNSUPPORTED
+    assert read(L, idx=FAKE, B=4, n=1 << 61) == INVALID
+    assert keys(L, B=1 << 30, S=(1 << 34), t_max=1 << 34, n_max=1 << 34, m=1) == UNSUPPORTED

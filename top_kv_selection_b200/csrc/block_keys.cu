@@ -158,9 +158,9 @@ block_keys_kernel(const uint8_t *__restrict__ k_cache, const float *__restrict__
 extern "C" dsa_status dsa_block_keys(const uint8_t *k_cache, const float *k_scale, int64_t t_max, int B,
                                      int64_t start_pos, int64_t S, int D, int block, uint8_t *blk_cache,
                                      float *blk_scale, int64_t n_max, dsa_stream_t stream) {
-    if (B < 0 || S < 0 || start_pos < 0 || block < 1 || n_max < 0) return DSA_ERR_INVALID_ARG;
+    if (B < 0 || S < 0 || start_pos < 0 || block < 1 || n_max < 0 || t_max < 0) return DSA_ERR_INVALID_ARG;
     if (D != 64 && D != 128) return DSA_ERR_UNSUPPORTED;
-    if (start_pos + S > t_max) return DSA_ERR_INVALID_ARG;
+    if (start_pos > t_max - S) return DSA_ERR_INVALID_ARG;
     const int64_t first = start_pos / block, last = (start_pos + S) / block;
     if (last > n_max) return DSA_ERR_INVALID_ARG;
     if (B == 0 || last == first) return DSA_OK;
@@ -168,9 +168,9 @@ extern "C" dsa_status dsa_block_keys(const uint8_t *k_cache, const float *k_scal
     if (!dsa::aligned16(k_cache) || !dsa::aligned16(blk_cache) || (reinterpret_cast<uintptr_t>(k_scale) & 3) ||
         (reinterpret_cast<uintptr_t>(blk_scale) & 3))
         return DSA_ERR_INVALID_ARG;
+    if (last - first > (int64_t)INT32_MAX * dsa::kWarps / B) return DSA_ERR_UNSUPPORTED;     // more than a grid
     const int64_t total = B * (last - first);
     const int64_t blocks = (total + dsa::kWarps - 1) / dsa::kWarps;
-    if (blocks > INT32_MAX) return DSA_ERR_UNSUPPORTED;
     const unsigned grid = (unsigned)blocks;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (D == 128)

@@ -534,12 +534,12 @@ extern "C" dsa_status dsa_latent_prologue(const void *kv, dsa_dtype x_dtype, int
                                           const float *norm_w, float eps, const float *rope_cs,
                                           int interleaved, int64_t start_pos, int64_t t_max,
                                           void *cache, dsa_dtype cache_dt, dsa_stream_t stream) {
-    if (B < 0 || S < 0 || start_pos < 0) return DSA_ERR_INVALID_ARG;
+    if (B < 0 || S < 0 || start_pos < 0 || t_max < 0) return DSA_ERR_INVALID_ARG;
     if (x_dtype != DSA_F32 && x_dtype != DSA_BF16) return DSA_ERR_INVALID_ARG;
     if (cache_dt != DSA_BF16 && cache_dt != DSA_FP8_LATENT && cache_dt != DSA_Q4_LATENT)
         return DSA_ERR_INVALID_ARG;
     if (!dsa::latent_shape_ok(dc, dr)) return DSA_ERR_UNSUPPORTED;
-    if (start_pos + S > t_max) return DSA_ERR_INVALID_ARG;
+    if (start_pos > t_max - S) return DSA_ERR_INVALID_ARG;
     if (B == 0 || S == 0) return DSA_OK;
     if (!kv || !cache) return DSA_ERR_INVALID_ARG;
     const int64_t per16 = x_dtype == DSA_BF16 ? 8 : 4;
@@ -581,9 +581,9 @@ extern "C" dsa_status dsa_latent_read(const void *cache, dsa_dtype cache_dt, int
     if (cache_dt != DSA_BF16 && cache_dt != DSA_FP8_LATENT && cache_dt != DSA_Q4_LATENT)
         return DSA_ERR_INVALID_ARG;
     if (!dsa::latent_shape_ok(dc, dr)) return DSA_ERR_UNSUPPORTED;
-    if (!idx && start_pos + n > t_max) return DSA_ERR_INVALID_ARG;
+    if (!idx && start_pos > t_max - n) return DSA_ERR_INVALID_ARG;
     if (B == 0 || n == 0) return DSA_OK;
-    if (t_max == 0) return DSA_ERR_INVALID_ARG;            // no row to name
+    if (t_max == 0 || n > INT64_MAX / B) return DSA_ERR_INVALID_ARG;     // no row to name; no such output
     if (!cache || !out || !dsa::aligned16(cache) || !dsa::aligned16(out) ||
         (reinterpret_cast<uintptr_t>(idx) & 3))
         return DSA_ERR_INVALID_ARG;
