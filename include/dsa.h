@@ -100,11 +100,14 @@ dsa_status dsa_get_device_error(dsa_stream_t stream, int32_t *device_status);
  * load, a tensor-core commit, a peer CTA) gives up after a budget of SM clock
  * cycles, records DSA_ERR_TIMEOUT in the device word above and lets the kernel
  * return normally: no trap, and the context stays usable.  This call launches
- * one CTA that waits through that same routine on a shared-memory barrier,
+ * one warp that waits through that same routine on a shared-memory barrier,
  * with a budget of budget_cycles (1 .. 2e9, about a second at 2 GHz, the
  * budget the kernels use).  With complete = 0 nobody arrives, so the wait
- * expires after about budget_cycles and DSA_ERR_TIMEOUT is recorded; with
- * complete != 0 the barrier completes at once and nothing is recorded.
+ * expires after about budget_cycles and DSA_ERR_TIMEOUT is recorded.  With
+ * complete = 2 one lane gives up early and the barrier completes right after:
+ * the warp gives up as one and DSA_ERR_TIMEOUT is recorded (DSA_ERR_DEVICE if
+ * its lanes went apart).  With any other value the barrier completes at once
+ * and nothing is recorded.
  * Returns DSA_ERR_INVALID_ARG for a budget outside that range (nothing
  * launched), DSA_ERR_CUDA if the launch fails.
  */

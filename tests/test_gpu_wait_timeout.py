@@ -64,3 +64,12 @@ def test_context_usable_after_expired_wait(dsa):
     dsa.dsa_topk_select(torch.from_numpy(np.ascontiguousarray(sc)).cuda(), T - 1, k, idx, ws)
     assert np.array_equal(idx.cpu().numpy(), oracle.topk_select(sc, T - 1, k))
     assert dsa.dsa_get_device_error() == dsa.DSA_OK
+
+
+def test_a_warp_gives_up_as_one(dsa):
+    """One lane's budget ends long before the others', and the barrier completes right after:
+    the lanes that see it complete leave with the lane that gave up (else DSA_ERR_DEVICE)."""
+    dsa.dsa_get_device_error()
+    for _ in range(20):
+        dsa.dsa_wait_selftest(1_000_000, complete=2)
+        assert dsa.dsa_get_device_error() == dsa.DSA_ERR_TIMEOUT

@@ -194,11 +194,12 @@ def dsa_get_device_error(stream=None) -> int:
     return code.value
 
 
-def dsa_wait_selftest(budget_cycles: int, complete: bool = False, stream=None) -> None:
+def dsa_wait_selftest(budget_cycles: int, complete: int = False, stream=None) -> None:
     """Run one bounded device wait of budget_cycles SM cycles: with complete=False
     nobody arrives, so it expires and records DSA_ERR_TIMEOUT (read it with
-    dsa_get_device_error); with complete=True it succeeds at once."""
-    _check("dsa_wait_selftest", _lib.dsa_wait_selftest(int(budget_cycles), 1 if complete else 0,
+    dsa_get_device_error); with complete=True it succeeds at once; with complete=2
+    the barrier completes after one lane of the warp has given up, and all give up."""
+    _check("dsa_wait_selftest", _lib.dsa_wait_selftest(int(budget_cycles), int(complete),
                                                        _stream(stream)))
 
 

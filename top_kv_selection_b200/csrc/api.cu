@@ -89,21 +89,37 @@ extern "C" dsa_status dsa_get_device_error(dsa_stream_t stream, int32_t *device_
 
 namespace {
 
-// One CTA waits on a shared-memory barrier through the wait routine every
-// kernel of the library uses, with the given budget; nobody arrives unless
-// `complete`, so the wait either succeeds at once or expires and records
-// DSA_ERR_TIMEOUT.
-__global__ void __launch_bounds__(32) wait_selftest_kernel(long long budget, int complete, int *err) {
+// One warp waits on a shared-memory barrier through the wait routine every
+// kernel of the library uses, and agrees on its outcome, with the given budget;
+// nobody arrives unless `complete`, so the wait either succeeds at once
+// or expires and records DSA_ERR_TIMEOUT.  With complete = 2 one lane's budget
+// is a sixteenth of the others' and the barrier completes once that lane has
+// given up: all lanes must give up with it (else DSA_ERR_DEVICE takes the
+// code's place).
+__global__ void __launch_bounds__(64) wait_selftest_kernel(long long budget, int complete, int *err) {
     __shared__ __align__(8) uint64_t bar;
     __shared__ int abort_flag;
+    volatile int *abort = &abort_flag;
+    const int lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         dsa::tc::mbar_init(&bar, 1);
         abort_flag = 0;
         dsa::tc::fence_mbar_init();
     }
     __syncthreads();
-    if (complete && threadIdx.x == 0) dsa::tc::mbar_arrive(&bar);
-    dsa::tc::mbar_wait(&bar, 0, err, &abort_flag, budget);
+    if (threadIdx.x < 32) {
+        if (complete == 1 && lane == 0) dsa::tc::mbar_arrive(&bar);
+        __syncwarp();
+        bool ok = dsa::tc::mbar_wait(&bar, 0, err, abort, complete == 2 && lane == 0 ? budget / 16 : budget);
+        ok = dsa::tc::warp_agrees(ok);
+        const uint32_t votes = __ballot_sync(0xffffffffu, ok);
+        if (lane == 0 && votes != 0 && votes != 0xffffffffu && err) atomicExch(err, DSA_ERR_DEVICE);
+    } else if (complete == 2 && lane == 0) {
+        const long long t0 = clock64();
+        while (!*abort && clock64() - t0 <= budget) {
+        }
+        dsa::tc::mbar_arrive(&bar);
+    }
     __syncthreads();
 }
 
@@ -111,9 +127,10 @@ __global__ void __launch_bounds__(32) wait_selftest_kernel(long long budget, int
 
 extern "C" dsa_status dsa_wait_selftest(int64_t budget_cycles, int complete, dsa_stream_t stream) {
     if (budget_cycles < 1 || budget_cycles > dsa::tc::kWaitBudget) return DSA_ERR_INVALID_ARG;
+    if (complete != 0 && complete != 2) complete = 1;
     int *err = dsa::device_error_word();
     if (!err) return DSA_ERR_CUDA;
-    wait_selftest_kernel<<<1, 32, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+    wait_selftest_kernel<<<1, 64, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
         (long long)budget_cycles, complete, err);
     return dsa::launch_status();
 }

@@ -547,17 +547,18 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
             const uint64_t vd0 = tc::smem_desc(tile, 1024, tc::kSwizzle128B, kRegion);
             const uint64_t pd0 = tc::smem_desc(pbase, 1024, tc::kSwizzle128B, kRegion);
             const int rope_steps = (a.dr + 15) / 16;
-            bool counted = one_tile;
+            // (a wait that gave up ends the walk at its tile's end, for all lanes
+            // at once: nothing before that branches on one lane's answer)
             ok = tc::mbar_wait(&ctl.q_full, 0, a.err, abort);
             tc::fence_proxy_async_smem();
-            for (int i = 0; ok && i < tiles; i++) {
+            for (int i = 0; i < tiles; i++) {
                 const uint32_t ph = i & 1;
                 // What is behind the barriers was written through the generic
                 // proxy (stores or cp.async); this warp's fence orders it before
                 // the MMAs' reads (one fence here costs less than one in each
                 // of the storing threads: 1007 against 1020 us at 1024 queries).
-                for (int m = 0; ok && m < mt; m++) {
-                    ok = tc::mbar_wait(&ctl.full[m], ph, a.err, abort);
+                for (int m = 0; m < mt; m++) {
+                    ok &= tc::mbar_wait(&ctl.full[m], ph, a.err, abort);
                     tc::fence_proxy_async_smem();
                     tc::tc_fence_after();
                     const uint64_t kd = kd0 + m * (2 * kRegion / 16), qd = qd0 + m * (2 * NH * 128 / 16);
@@ -569,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
                     }
                     __syncwarp();
                 }
-                if (!ok || !(ok = tc::mbar_wait(&ctl.full[4], ph, a.err, abort))) break;
+                ok &= tc::mbar_wait(&ctl.full[4], ph, a.err, abort);
                 tc::fence_proxy_async_smem();
                 tc::tc_fence_after();
                 if (tc::elect_one()) {
@@ -581,11 +582,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
                 __syncwarp();
                 if (i == 0 && !one_tile) {
                     tc::named_barrier(2, kThreads);
-                    counted = true;
                     const int last = __shfl_sync(0xffffffffu, ctl.last, 0);
                     tiles = last < lo ? 1 : (last - lo) / kTile + 1;
                 }
-                if (!(ok = tc::mbar_wait(&ctl.p_full, ph, a.err, abort))) break;
+                ok &= tc::mbar_wait(&ctl.p_full, ph, a.err, abort);
                 tc::fence_proxy_async_smem();
                 tc::tc_fence_after();
                 // step x: slots [16 x, 16 x + 16) of the chunk pair (A, two
@@ -600,18 +600,21 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
                         tc::tc_commit(&ctl.o_done[m]);
                     }
                 }
-                __syncwarp();
+                if (!tc::warp_agrees(ok)) break;
             }
-            if (!counted) tc::named_barrier(2, kThreads);   // (a wait gave up before the count)
-            // every issued MMA completes before TMEM is released
+            // every issued MMA completes before TMEM is released, after a wait
+            // that gave up too (this one does not look at the others' flag)
             if (tc::elect_one()) tc::tc_commit(&ctl.mma_fin);
             __syncwarp();
-            tc::mbar_wait(&ctl.mma_fin, 0, a.err, abort);
+            int alone = 0;
+            tc::mbar_wait(&ctl.mma_fin, 0, a.err, &alone);
         }
         __syncwarp();
     }
     // ------------------------------------------------------------ epilogue
     if (warp < kWork / 32) {
+        // (none is in flight unless a wait gave up)
+        asm volatile("cp.async.wait_all;" ::: "memory");
         tc::named_barrier(3, kWork);
         // thread = (column of dc, quarter of the heads): a warp stores 32
         // consecutive columns of one head at a time
@@ -624,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
                 ld_cols(tmem + ((uint32_t)(q4 * 32) << 16) + NH * (m + 1) + c * kCols, v);
                 tc::tmem_wait_ld();
                 const int col = m * 128 + q4 * 32 + lane;
-                const int n = ok ? heads - c * kCols : 0;   // heads of this thread
+                const int n = ok && !*abort ? heads - c * kCols : 0;   // heads of this thread
                 if (a.splits > 1) {
                     float *o = a.part_o + ((int64_t)blockIdx.x * NH + c * kCols) * a.dc + col;
 #pragma unroll

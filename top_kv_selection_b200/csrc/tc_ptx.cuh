@@ -102,6 +102,12 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, int *e
     }
 }
 
+// Whether all lanes of a warp got through their waits.  Each lane polls for
+// itself, so that one can give up where another still sees the phase complete;
+// a warp that goes on to warp-wide instructions (elect.sync, a named barrier,
+// tcgen05) must not branch on a lane's own answer but on this one.
+__device__ __forceinline__ bool warp_agrees(bool ok) { return __all_sync(0xffffffffu, ok); }
+
 // ------------------------------------------------------ thread-block clusters
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
