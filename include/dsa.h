@@ -395,8 +395,10 @@ dsa_status dsa_sparse_mla_attn_q4(const void *q, const uint8_t *kv_q4, int64_t t
  * dsa_block_keys: the keys of the blocks that the tokens start_pos ..
  * start_pos + S - 1 finish (block e is the tokens [e block, (e + 1) block)).  A
  * block's key is the mean of its tokens' decoded keys (code * scale), quantised
- * as dsa_indexer_quant quantises a rotated vector; codes are those of the exact
- * mean (taken again in 64 bits where fp32 leaves them in doubt).
+ * as dsa_indexer_quant quantises a rotated vector.  Codes are those of the exact
+ * mean over the exact scale, also where tokens cancel (they are taken again in 64
+ * bits where the error of fp32 sums of such terms leaves them in doubt); blk_scale
+ * is off by at most 2^-14 of itself.
  *   k_cache [B,t_max,D] e4m3, k_scale [B,t_max] fp32: the indexer's key cache,
  *           the new tokens' keys already appended
  *   blk_cache [B,n_max,D] e4m3, blk_scale [B,n_max] fp32: entry e is written for

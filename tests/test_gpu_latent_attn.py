@@ -434,6 +434,73 @@ def test_block_keys_do_not_depend_on_how_the_tokens_arrive(dsa):
     assert t == T and torch.equal(whole[0], steps[0]) and torch.equal(whole[1], steps[1])
 
 
+def exact_codes(mean, scale):
+    """Values of the e4m3 codes nearest to mean / scale (ties to even), and which quotients lie
+    within 2^-40 of a border between two codes (beyond what 64-bit sums can tell)."""
+    q = mean / scale
+    step = np.exp2(np.maximum(np.floor(np.log2(np.maximum(np.abs(q), 2.0 ** -30))), -6) - 3)
+    n = q / step
+    near = np.abs(np.abs(n - np.floor(n)) - 0.5) < np.maximum(np.abs(n), 1) * 2.0 ** -40
+    return np.clip(np.rint(n) * step, -448, 448), near
+
+
+@pytest.mark.parametrize("D", [128, 64])
+@pytest.mark.parametrize("block", [4, 16, 64, 130, 512])
+@pytest.mark.parametrize("eps", [None, 1e-2, 1e-3, 1e-4, 0.0])
+def test_block_keys_of_tokens_that_cancel(dsa, D, block, eps):
+    """Pairs of tokens of opposite sign whose scales differ by a relative eps: the mean is eps of
+    its terms (eps 0: none is left; None: ordinary keys).  Codes are those of the 64-bit mean; a
+    term's product is exact in 64 bits and a sum of 512 off by at most 512 * 2^-53 of its
+    largest terms, 2^-30 of the mean at eps 1e-4, so that far fewer dims than one in a run are
+    within that of a border: a dim that is may differ."""
+    n = 120 if block < 100 else 24
+    g = torch.Generator().manual_seed(block + D)
+    kc = torch.randint(0, 127, (1, n * block, D), generator=g, dtype=torch.uint8)
+    ks = torch.rand(1, n * block, generator=g) + 0.5
+    if eps is None:
+        kc |= torch.randint(0, 2, kc.shape, generator=g, dtype=torch.uint8) << 7
+    else:
+        kc[:, 1::2] = kc[:, ::2] | 0x80
+        ks[:, 1::2] = ks[:, ::2] * (1 + eps)
+    kc[0, -block:] = 0                                   # a block of zeros
+    kc[0, -3 * block:-2 * block] &= 0x80                 # and of zeros of either sign
+    ks[0, -5 * block:-4 * block] *= 1e-9                 # and one under the scale's floor
+    bc, bs = torch.zeros(1, n, D, dtype=torch.uint8, device="cuda"), torch.zeros(1, n, device="cuda")
+    dsa.dsa_block_keys(kc.cuda(), ks.cuda(), 0, n * block, block, bc, bs)
+    k = (R.E4M3[kc[0].numpy()] * ks[0].double().numpy()[:, None]).astype(np.longdouble)
+    mean = k.reshape(n, block, D).sum(1).astype(np.float64) / block
+    scale = np.maximum(np.abs(mean).max(-1), np.float64(np.float32(1e-4))) / 448
+    got_s = bs[0].double().cpu().numpy()
+    assert np.all(np.abs(got_s - scale) <= scale * 2.0 ** -14)
+    want, near = exact_codes(mean, scale[:, None])
+    if eps == 1e-4:
+        near |= np.abs(exact_codes(mean * (1 + 2.0 ** -30), scale[:, None])[0] -
+                       exact_codes(mean * (1 - 2.0 ** -30), scale[:, None])[0]) > 0
+    assert near.mean() < 1e-3 or block <= 16
+    assert np.all((R.E4M3[bc[0].cpu().numpy()] == want) | near)
+
+
+def test_block_keys_keep_nan_and_sums_past_fp32(dsa):
+    """A NaN code makes its dim NaN and no other; terms whose fp32 sum would pass the type's
+    range keep their mean."""
+    D, block = 128, 16
+    kc = torch.randint(0, 126, (1, 3 * block, D), generator=torch.Generator().manual_seed(3), dtype=torch.uint8)
+    ks = torch.full((1, 3 * block), 0.5)
+    kc[0, 5, 77] = 0xFF
+    ks[0, block:2 * block] = 7e35                        # 448 * 7e35 = 3.1e38, times 16
+    bc, bs = torch.zeros(1, 3, D, dtype=torch.uint8, device="cuda"), torch.zeros(1, 3, device="cuda")
+    dsa.dsa_block_keys(kc.cuda(), ks.cuda(), 0, 3 * block, block, bc, bs)
+    got = R.E4M3[bc[0].cpu().numpy()]
+    assert np.isnan(got[0, 77])
+    mean = (R.E4M3[kc[0].numpy()] * ks[0].double().numpy()[:, None]).reshape(3, block, D).mean(1)
+    scale = np.nanmax(np.abs(mean), -1) / 448
+    assert np.all(np.abs(bs[0].double().cpu().numpy() - scale) <= scale * 2.0 ** -14)
+    want, near = exact_codes(np.nan_to_num(mean), scale[:, None])
+    ok = (got == want) | near
+    ok[0, 77] = True
+    assert ok.all()
+
+
 # ------------------------------------------------------------ operators together
 def test_decode_step_over_the_4_bit_cache(dsa):
     """dsa_decode_step with a 4-bit latent cache whose newest row the prologue wrote: the

@@ -9,11 +9,20 @@
 // A warp owns a block: one 16-byte load gives a lane 16 dims of a token, so
 // D / 16 lanes cover a token and a warp 512 / D tokens per load.  Each lane
 // sums its dims over its tokens in fp32 (packed pairs, up to sixteen tokens'
-// loads in flight: 138 MB of keys take 29.7 us; eight at a time cost 3 more); the lanes of a token group then trade halves until each holds the
-// sums of D / 32 dims, in a fixed order.  Codes that the fp32 mean leaves in
-// doubt are taken from a mean in 64 bits (about one block in 30).  The keys'
-// bytes (D + 4 per token) bound it from below; the decoding of the codes, some
-// ten instructions a token and warp, comes close.
+// loads in flight); the lanes of a token group then trade halves until each
+// holds the sums of D / 32 dims, in a fixed order.
+//
+// An fp32 sum's error goes by its terms and not by what is left of them when
+// tokens cancel, so the warp carries a bound on the terms, from the scales
+// alone, and takes dims whose code that leaves in doubt again in 64 bits: at 64
+// random tokens a block, about one dim in every third block.  Where the bound
+// passes 2^-14 of the largest dim, the scale's dim is among them.  138 MB of
+// keys in blocks of 64 tokens take 30.2 us, in blocks of 128 29.3, of 16 43.5,
+// of 2048 230 (there all blocks are summed twice); sums in 64 bits throughout
+// (two more integer instructions a code) took 38, 40 and 80 us at 64, at 64 with
+// all loads ahead, and at 2048.  The keys' bytes (D + 4 per token) bound it from
+// below; the decoding of the codes, some ten instructions a token and warp,
+// comes close.
 #include <type_traits>
 
 #include "common.cuh"
@@ -22,10 +31,20 @@
 namespace dsa {
 namespace {
 
-constexpr int kWarps = 8;
+// A warp that takes dims again holds its block's place: two warps a block 30.2, eight
+// 34.1 us (138 MB, 64 tokens a block).
+constexpr int kWarps = 2;
+constexpr int kFew = 16;         // dims that are worth a round of eight lanes each
+
+// x as fp32 for the rounding to a code: cut, with a bit that says so, so that the
+// code is that of x (not of x rounded to fp32 first).
+__device__ __forceinline__ float f32_odd(double x) {
+    const float f = __double2float_rz(x);
+    return (double)f == x ? f : __uint_as_float(__float_as_uint(f) | 1u);
+}
 
 template <int D>
-__global__ void __launch_bounds__(32 * kWarps, 3)
+__global__ void __launch_bounds__(32 * kWarps, 16)
 block_keys_kernel(const uint8_t *__restrict__ k_cache, const float *__restrict__ k_scale, int64_t t_max, int64_t first,
                   int64_t per_seq, int64_t total, int block, uint8_t *__restrict__ blk_cache,
                   float *__restrict__ blk_scale, int64_t n_max) {
@@ -40,8 +59,12 @@ block_keys_kernel(const uint8_t *__restrict__ k_cache, const float *__restrict__
     float2 acc[8];
 #pragma unroll
     for (int d = 0; d < 8; d++) acc[d] = make_float2(0.f, 0.f);
+    // of the scales: the sum, and the sum of the partial sums (the error's bound)
+    float sum_s = 0.f, sum_p = 0.f;
     auto add = [&](const uint4 &w, float s) {
         const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+        sum_s += fabsf(s);
+        sum_p += sum_s;
 #pragma unroll
         for (int q = 0; q < 4; q++) {
             float f[4];
@@ -98,57 +121,122 @@ block_keys_kernel(const uint8_t *__restrict__ k_cache, const float *__restrict__
         amax = fmaxf(amax, fabsf(v[d]));
     }
     amax = warp_max(amax);
+    // How far the fp32 means may be off.  A term is at most 448 of its scale, so a
+    // lane's partial sums are at most 448 of its scales' partial sums, and each step
+    // is off by 2^-24 of one; a trade by 2^-24 of the sum so far, as are the two
+    // roundings of the mean.  (A sixteenth more for the roundings of the bound.)
+    constexpr int kTrades = kTok == 8 ? 3 : 2;
+    float err = sum_p + (kTrades + 2) * sum_s;
+#pragma unroll
+    for (int m = 16; m >= kLanes; m >>= 1) err += __shfl_xor_sync(0xffffffffu, err, m);
+    err *= inv * (448.f * 0x1.1p-24f);
     float sc = __fdiv_rn(fmaxf(amax, 1e-4f), 448.0f);
     const float rs = __frcp_rn(sc);
-    // A quotient is in doubt when its fp32 error may reach over a border between
-    // two codes: 2^-21 of the vector's largest (448), since the sum's error goes
-    // by its terms and not by what they cancel to, and 2^-20 of itself.
-    constexpr float kAbs = 448.f * 0x1p-21f;
-    uint32_t lo = 0, hi = 0;
+    // A code is in doubt where that error, of the mean and of the scale, may reach
+    // over a border (a zero's sign does not count); a dim may be the largest where it
+    // reaches the largest, which the scale's floor may make idle.  (Comparisons are
+    // such that NaN, and a sum that leaves fp32's range, put a dim in doubt.)
+    float far = err * rs;
+    far = fmaf(far, far * (2.f / 448.f), far);
+    const float rel = fmaf(far, 1.f / 448.f, 0x1p-21f);
+    const bool floor = amax + 2.f * err < 1e-4f;
+    uint32_t codes = 0, todo = 0;
 #pragma unroll
     for (int d = 0; d < kOwn; d += 2) {
         const float q0 = v[d] * rs, q1 = v[d + 1] * rs;
-        const float d0 = fmaf(fabsf(q0), 0x1p-20f, kAbs), d1 = fmaf(fabsf(q1), 0x1p-20f, kAbs);
-        lo |= e4m3x2_rn_sat(q0 - d0, q1 - d1) << (8 * d);
-        hi |= e4m3x2_rn_sat(q0 + d0, q1 + d1) << (8 * d);
+        const float d0 = fmaf(fabsf(q0), rel, far), d1 = fmaf(fabsf(q1), rel, far);
+        const uint32_t lo = e4m3x2_rn_sat(q0 - d0, q1 - d1), hi = e4m3x2_rn_sat(q0 + d0, q1 + d1);
+        const uint32_t off = lo ^ hi, mag = (lo | hi) & 0x7F7F;
+        codes |= e4m3x2_rn_sat(q0, q1) << (8 * d);
+        todo |= (uint32_t)((off & 0xFF) && (mag & 0xFF)) << d;
+        todo |= (uint32_t)((off >> 8) && (mag >> 8)) << (d + 1);
     }
-    if (__any_sync(0xffffffffu, lo != hi)) {
+    if (__any_sync(0xffffffffu, todo != 0 || !(floor || (err < amax * 0x1p-14f && amax < INFINITY)))) {
+        // Those dims in 64 bits, and the largest one for the scale.
+        const float least = amax == INFINITY ? 0.f : floor ? INFINITY : amax - 2.125f * err;
+        uint32_t left[kOwn];
+        int n = 0;
         double x[kOwn], top = 0.0;
 #pragma unroll
-        for (int d = 0; d < kOwn; d++) x[d] = 0.0;
-        const uint8_t *k0 = k_cache + t0 * D + own;
-#pragma unroll 16
-        for (int t = 0; t < block; t++) {
-            const double s = (double)k_scale[t0 + t];
-            uint32_t w;
-            if constexpr (kOwn == 4)
-                w = *reinterpret_cast<const uint32_t *>(k0 + (int64_t)t * D);
-            else
-                w = *reinterpret_cast<const uint16_t *>(k0 + (int64_t)t * D);
-            float f[4];
-            e4m3x4_to_f32(w, f[0], f[1], f[2], f[3]);
-#pragma unroll
-            for (int d = 0; d < kOwn; d++) x[d] = fma((double)f[d], s, x[d]);
-        }
-#pragma unroll
         for (int d = 0; d < kOwn; d++) {
-            x[d] /= block;
-            top = fmax(top, fabs(x[d]));
+            todo |= (uint32_t)!(fabsf(v[d]) < least) << d;
+            left[d] = __ballot_sync(0xffffffffu, todo >> d & 1);
+            n += __popc(left[d]);
+            x[d] = 0.0;
+        }
+        if (n > kFew) {
+            // many: every lane its own dims
+            todo = (1u << kOwn) - 1;
+            const uint8_t *k0 = k_cache + t0 * D + own;
+#pragma unroll 16
+            for (int t = 0; t < block; t++) {
+                const double s = (double)k_scale[t0 + t];
+                uint32_t w;
+                if constexpr (kOwn == 4)
+                    w = *reinterpret_cast<const uint32_t *>(k0 + (int64_t)t * D);
+                else
+                    w = *reinterpret_cast<const uint16_t *>(k0 + (int64_t)t * D);
+                float f[4];
+                e4m3x4_to_f32(w, f[0], f[1], f[2], f[3]);
+#pragma unroll
+                for (int d = 0; d < kOwn; d++) x[d] = fma((double)f[d], s, x[d]);
+            }
+#pragma unroll
+            for (int d = 0; d < kOwn; d++) x[d] /= block;
+            n = 0;
+        }
+        // few: four at a time, eight lanes a dim, a lane every eighth token
+        for (; n > 0; n -= 4) {
+            int who = -1;                                  // the lane that has the group's dim | d << 8
+#pragma unroll
+            for (int g = 0; g < 4; g++) {
+                int pick = -1;
+#pragma unroll
+                for (int d = 0; d < kOwn; d++) {
+                    if (pick < 0 && left[d]) {
+                        pick = (__ffs(left[d]) - 1) | d << 8;
+                        left[d] &= left[d] - 1;
+                    }
+                }
+                if (lane >> 3 == g) who = pick;
+            }
+            const int dim = __shfl_sync(0xffffffffu, own, who & 31) + (who >> 8);
+            double y = 0.0;
+            if (who >= 0) {
+                const uint8_t *k0 = k_cache + t0 * D + dim;
+#pragma unroll 8
+                for (int t = lane & 7; t < block; t += 8)
+                    y = fma((double)e4m3_to_f32(k0[(int64_t)t * D]), (double)k_scale[t0 + t], y);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int m = 4; m > 0; m >>= 1) y += __shfl_xor_sync(0xffffffffu, y, m);
+            y /= block;
+#pragma unroll
+            for (int g = 0; g < 4; g++) {
+                const int to = __shfl_sync(0xffffffffu, who, 8 * g);
+                const double z = __shfl_sync(0xffffffffu, y, 8 * g);
+#pragma unroll
+                for (int d = 0; d < kOwn; d++)
+                    if (to == (lane | d << 8)) x[d] = z;
+            }
         }
 #pragma unroll
-        for (int m = 1; m < 32; m <<= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, m));
+        for (int d = 0; d < kOwn; d++) top = fmax(top, fabs(x[d]));
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, m));
         const double exact = fmax(top, (double)1e-4f) / 448.0;
         sc = __double2float_rn(exact);
-        lo = 0;
 #pragma unroll
-        for (int d = 0; d < kOwn; d += 2)
-            lo |= e4m3x2_rn_sat(__double2float_rn(x[d] / exact), __double2float_rn(x[d + 1] / exact)) << (8 * d);
+        for (int d = 0; d < kOwn; d++) {
+            if (todo >> d & 1) codes = (codes & ~(0xFFu << (8 * d))) | (e4m3x2_rn_sat(f32_odd(x[d] / exact), 0.f) & 0xFF) << (8 * d);
+        }
     }
     uint8_t *dst = blk_cache + (b * n_max + e) * D + own;
     if constexpr (kOwn == 4)
-        *reinterpret_cast<uint32_t *>(dst) = lo;
+        *reinterpret_cast<uint32_t *>(dst) = codes;
     else
-        *reinterpret_cast<uint16_t *>(dst) = (uint16_t)lo;
+        *reinterpret_cast<uint16_t *>(dst) = (uint16_t)codes;
     if (lane == 0) blk_scale[b * n_max + e] = sc;
 }
 
