@@ -403,7 +403,8 @@ dsa_status dsa_sparse_mla_attn_q4(const void *q, const uint8_t *kv_q4, int64_t t
  *           the new tokens' keys already appended
  *   blk_cache [B,n_max,D] e4m3, blk_scale [B,n_max] fp32: entry e is written for
  *           every finished block, nothing else; (start_pos + S) / block <= n_max
- * D 64 or 128; k_cache and blk_cache 16-byte aligned.
+ * D 64 or 128, block up to 2^20 (else DSA_ERR_UNSUPPORTED); k_cache and blk_cache
+ * 16-byte aligned.
  */
 dsa_status dsa_block_keys(const uint8_t *k_cache, const float *k_scale, int64_t t_max, int B,
                           int64_t start_pos, int64_t S, int D, int block, uint8_t *blk_cache,

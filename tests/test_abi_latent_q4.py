@@ -178,3 +178,11 @@ def test_row_counts_past_64_bits_are_refused(dsa):
         assert attn(dsa, blocks, B=1 << 30, S=1 << 30, Hq=16, sp=0, t_max=(1 << 31) - 1, k=16) == UNSUPPORTED
     assert read(L, idx=FAKE, B=4, n=1 << 61) == INVALID
     assert keys(L, B=1 << 30, S=(1 << 34), t_max=1 << 34, n_max=1 << 34, m=1) == UNSUPPORTED
+
+
+def test_block_keys_refuse_blocks_past_their_counters(dsa):
+    """A block near 2^31 tokens would take the kernel's token counter past 32 bits."""
+    for m in ((1 << 20) + 1, (1 << 31) - 1, (1 << 31) - 100):
+        assert keys(dsa._lib, m=m, t_max=1 << 32, S=1 << 32) == UNSUPPORTED
+        assert keys(dsa._lib, m=m, t_max=1 << 32, S=1, D=64) == UNSUPPORTED
+    assert keys(dsa._lib, m=1 << 20, k=NULL, S=(1 << 20) - 1, t_max=1 << 20) == OK      # finishes no block

@@ -248,6 +248,9 @@ extern "C" dsa_status dsa_block_keys(const uint8_t *k_cache, const float *k_scal
                                      float *blk_scale, int64_t n_max, dsa_stream_t stream) {
     if (B < 0 || S < 0 || start_pos < 0 || block < 1 || n_max < 0 || t_max < 0) return DSA_ERR_INVALID_ARG;
     if (D != 64 && D != 128) return DSA_ERR_UNSUPPORTED;
+    // (the kernel counts a block's tokens in 32 bits, sixteen loads ahead, and the
+    // error's bound has room for the roundings of this many)
+    if (block > 1 << 20) return DSA_ERR_UNSUPPORTED;
     if (start_pos > t_max - S) return DSA_ERR_INVALID_ARG;
     const int64_t first = start_pos / block, last = (start_pos + S) / block;
     if (last > n_max) return DSA_ERR_INVALID_ARG;
