@@ -339,9 +339,9 @@ int64_t dsa_latent_q4_row_bytes(int dc, int dr);
  *   p' = p rotated by rope_cs[s]                  (rope_cs NULL: p' = p)
  * then one rounding into row start_pos + s of the cache: bf16, the FP8 row
  * (dsa_latent_quant's rounding) or the 4-bit row.  bf16 and 4-bit rows hold the
- * rounding of the exact value (fp32 where that leaves no doubt, else 64 bits),
- * FP8 rows that of the fp32 one.  interleaved != 0 pairs elements (2j, 2j + 1) as
- * (re, im), 0 pairs (j, j + dr/2).
+ * rounding of the exact value (fp32 where that leaves no doubt, else 64 bits; bf16
+ * numbers, 4-bit scales among them, through fp32), FP8 rows that of the fp32 one.
+ * interleaved != 0 pairs elements (2j, 2j + 1) as (re, im), 0 pairs (j, j + dr/2).
  *
  *   kv       vector (b, s) at kv + b * batch_stride + s * token_stride (strides
  *            in elements of x_dtype, F32 or BF16; both multiples of 16 bytes,

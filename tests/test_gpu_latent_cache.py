@@ -199,6 +199,73 @@ def test_append_rounds_from_the_exact_value(dsa, S):
         assert np.all((got[..., :dc] == R.bf16(n * step)) | near)
 
 
+def q4_scales(y):
+    """The 4-bit scales of y [..., dc] in 64 bits: amax / 7 rounded to fp32, then to bf16."""
+    amax = np.abs(y.reshape(*y.shape[:-1], -1, 32)).max(-1)
+    return R.bf16((np.maximum(amax, np.float64(np.float32(1e-4))) / 7).astype(np.float32))
+
+
+def near_half(x):
+    """Quotients within 2^-40 of a border between two codes."""
+    return np.abs(np.abs(x - np.floor(x)) - 0.5) < 2.0 ** -40
+
+
+@pytest.mark.parametrize("dc", [512, 384, 128])
+def test_append_of_groups_next_to_a_border_of_their_scale(dsa, dc):
+    """fp32 rows of one magnitude (the sum's roundings add up), each group's largest value moved
+    to within six fp32 units of a border between two bf16 scales: the scale is the exact one."""
+    rows = 512 * 65536 // dc // 8
+    g = np.random.default_rng(dc)
+    for it in range(4):
+        x = (1 + 0.02 * g.random((rows, dc))) * g.choice([-1.0, 1.0], (rows, dc)) * g.uniform(0.5, 2, (rows, 1))
+        w = (1 + 0.3 * g.random(dc)).astype(np.float32)
+        at = np.arange(0, dc, 32) + g.integers(0, 32, dc // 32)
+        w[at] *= 1.5                                     # each group's largest
+        for _ in range(4):                               # (the norm moves a little with it)
+            x = x.astype(np.float32).astype(np.float64)
+            r = 1 / np.sqrt((x * x).mean(-1, keepdims=True) + 1e-6)
+            s = np.abs(x[:, at]) * r * w[at] / 7
+            m, e = np.frexp(s)
+            mid = np.ldexp((np.floor(m * 256) + 0.5) / 256, e)
+            x[:, at] *= mid / s * (1 + g.uniform(-6, 6, s.shape) * 2.0 ** -23 / (2 * m))
+        kv = torch.from_numpy(x.astype(np.float32))[None].contiguous()
+        cache = new_cache(1, rows, R.Q4, dc, 0)
+        dsa.dsa_latent_prologue(kv.cuda(), torch.from_numpy(w).cuda(), 1e-6, None, False, 0, cache, R.Q4, dc)
+        raw = to_bytes(cache)[0]
+        y = R.prologue(kv[0].double().numpy(), w.astype(np.float64), np.float64(np.float32(1e-6)), None, False, dc)
+        s = q4_scales(y)
+        lo = dc // 2
+        got = R._u16_as_bf16(raw[:, lo:lo + dc // 16:2], raw[:, lo + 1:lo + dc // 16:2])
+        assert np.array_equal(got, s), int((got != s).sum())
+        quot = y / np.repeat(s, 32, -1)
+        same = R.decode_rows(raw, R.Q4, dc, 0) == R.bf16(np.clip(np.rint(quot), -7, 7) * np.repeat(s, 32, -1))
+        assert np.all(same | near_half(quot))
+
+
+@pytest.mark.parametrize("fmt", [R.BF16, R.Q4])
+def test_append_of_values_and_weights_far_apart(dsa, fmt):
+    """Small values beside ordinary ones under weights far from one: no product on the way to
+    the rounding loses its last bits (or all of them) to fp32's range."""
+    dc, B, S = 256, 4, 8
+    g = torch.Generator().manual_seed(9)
+    kv = make_kv(B, S, dc, 0, torch.float32, 9, spread=False) * 2.0 ** -35
+    kv[..., 1::4] *= 2.0 ** -50
+    for lo, hi in ((2.0 ** -50, 2.0 ** 50), (2.0 ** -75, 2.0 ** 90), (1.0, 1.0)):
+        w = 1 + 0.2 * torch.randn(dc, generator=g)
+        w[1::4] *= lo
+        w[2::4] *= hi
+        cache = new_cache(B, S, fmt, dc, 0)
+        dsa.dsa_latent_prologue(kv.cuda(), w.cuda(), 0.0, None, False, 0, cache, fmt, dc)
+        got = R.decode_rows(to_bytes(cache), fmt, dc, 0)
+        y = R.prologue(kv.double().numpy(), w.double().numpy(), 0.0, None, False, dc)
+        if fmt == R.BF16:
+            # (torch's cast: R.bf16 has no subnormal numbers, and some of these are)
+            assert np.array_equal(got, torch.from_numpy(y).float().bfloat16().double().numpy())
+        else:
+            step = np.repeat(q4_scales(y), 32, -1)
+            assert np.all((got == R.bf16(np.clip(np.rint(y / step), -7, 7) * step)) | near_half(y / step))
+
+
 @pytest.mark.parametrize("fmt", [R.BF16, R.Q4])
 def test_append_of_extreme_and_nan_rows(dsa, fmt):
     """Rows whose squares leave fp32's range (with and without eps) keep the exact norm; a NaN

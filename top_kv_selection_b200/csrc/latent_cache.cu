@@ -19,8 +19,9 @@
 // Rounding.  What is stored is the rounding of the exact value (of the products
 // and the norm taken in 64 bits): the fp32 result is used where its error leaves
 // the rounded value in no doubt, and a row (or a rotary pair) where it might not,
-// about three 4-bit rows in a thousand, is taken again in 64 bits.  (FP8 codes of
-// a normed row are rounded from fp32.)
+// about sixteen 4-bit rows in a thousand, is taken again in 64 bits.  bf16 numbers
+// and 4-bit scales are rounded to fp32 first, then to bf16, like every cast of an
+// fp32 result.  (FP8 codes of a normed row are rounded from fp32.)
 #include <algorithm>
 
 #include "latent_rows.cuh"
@@ -127,41 +128,83 @@ __device__ __forceinline__ uint32_t q4_word(const float2 *r) {          // four 
     return w;
 }
 
-// A latent row's rounding in 64 bits, by the whole warp: lane = values lane,
-// lane + 32, ... (a 4-bit group at a time).  It runs for few rows; a function of
-// its own keeps its registers out of the common path.
+// A latent row's rounding in 64 bits, by the whole warp: lane = values 16 lane ..
+// 16 lane + 15, half a 4-bit group.  It runs for few rows; a function of its own
+// keeps its registers out of the common path.  (With the group over a warp's lanes
+// its exchanges took 6.5 us a row.)
 template <int F, typename T>
 __device__ __noinline__ void exact_row(const T *src, uint8_t *dst, const float *w, float eps, int dc, int dr) {
     const int lane = threadIdx.x & 31;
-    double x[16], ss = 0.0;
+    const bool on = 16 * lane < dc;
+    float2 f[8];
 #pragma unroll
-    for (int i = 0; i < 16; i++) {
-        x[i] = 32 * i < dc ? (double)to_f32<T>(src[32 * i + lane]) : 0.0;
-        ss = fma(x[i], x[i], ss);
-    }
+    for (int i = 0; i < 8; i++) f[i] = splat(0.f);
+    if (on) {
+        if constexpr (sizeof(T) == 2) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const double r = 1.0 / sqrt(ss / dc + (double)eps);
-#pragma unroll 4
-    for (int i = 0; i < 16; i++) {
-        if (32 * i >= dc) break;
-        const int d = 32 * i + lane;
-        const double y = x[i] * r * (double)w[d];
-        if constexpr (F == DSA_Q4_LATENT) {
-            double amax = fabs(y);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) amax = fmax(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            float sf = __double2float_rn(fmax(amax, (double)1e-4f) / 7.0);
-            if (__any_sync(0xffffffffu, y != y)) sf = __int_as_float(0x7FC00000);   // a NaN makes the group NaN
-            const __nv_bfloat16 sb = __float2bfloat16_rn(sf);
-            const int v = d & 7, n = max(-7, min(7, __double2int_rn(y / (double)__bfloat162float(sb))));
-            uint32_t code = (uint32_t)(8 + n) << (4 * (v / 2 + 4 * (v & 1)));
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) code |= __shfl_xor_sync(0xffffffffu, code, o);
-            if (v == 0) reinterpret_cast<uint32_t *>(dst)[d >> 3] = code;
-            if (lane == 0) reinterpret_cast<__nv_bfloat16 *>(dst + latent_q4_scales_at(dc, dr))[d >> 5] = sb;
+            for (int i = 0; i < 2; i++) {
+                const uint4 c = reinterpret_cast<const uint4 *>(src + 16 * lane)[i];
+                f[4 * i] = bf16x2_to_f32(c.x);
+                f[4 * i + 1] = bf16x2_to_f32(c.y);
+                f[4 * i + 2] = bf16x2_to_f32(c.z);
+                f[4 * i + 3] = bf16x2_to_f32(c.w);
+            }
         } else {
-            reinterpret_cast<__nv_bfloat16 *>(dst)[d] = __float2bfloat16_rn(__double2float_rn(y));
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const float4 c = reinterpret_cast<const float4 *>(src + 16 * lane)[i];
+                f[2 * i] = make_float2(c.x, c.y);
+                f[2 * i + 1] = make_float2(c.z, c.w);
+            }
+        }
+    }
+    double y[16], s0 = 0.0, s1 = 0.0;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        y[2 * i] = (double)f[i].x;
+        y[2 * i + 1] = (double)f[i].y;
+        s0 = fma(y[2 * i], y[2 * i], s0);
+        s1 = fma(y[2 * i + 1], y[2 * i + 1], s1);
+    }
+    s0 += s1;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+    const double r = 1.0 / sqrt(s0 / dc + (double)eps);
+    double amax = 0.0;
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const float4 wv = reinterpret_cast<const float4 *>(w)[on ? 4 * lane + i : 0];
+        const float wf[4] = {wv.x, wv.y, wv.z, wv.w};
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            y[4 * i + e] = y[4 * i + e] * r * (double)wf[e];
+            amax = fmax(amax, fabs(y[4 * i + e]));
+            nan |= y[4 * i + e] != y[4 * i + e];
+        }
+    }
+    if constexpr (F == DSA_Q4_LATENT) {
+        amax = fmax(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        const uint32_t bad = __ballot_sync(0xffffffffu, nan);
+        float sf = __double2float_rn(fmax(amax, (double)1e-4f) / 7.0);
+        if (bad >> (lane & 30) & 3) sf = __int_as_float(0x7FC00000);       // a NaN makes the group NaN
+        const __nv_bfloat16 sb = __float2bfloat16_rn(sf);
+        const double inv = 1.0 / (double)__bfloat162float(sb);
+        uint32_t c[2] = {0, 0};
+#pragma unroll
+        for (int v = 0; v < 16; v++)
+            c[v >> 3] |= (uint32_t)(8 + max(-7, min(7, __double2int_rn(y[v] * inv)))) << (4 * ((v & 7) / 2 + 4 * (v & 1)));
+        if (on) reinterpret_cast<uint2 *>(dst)[lane] = make_uint2(c[0], c[1]);
+        if (on && (lane & 1) == 0)
+            reinterpret_cast<__nv_bfloat16 *>(dst + latent_q4_scales_at(dc, dr))[lane >> 1] = sb;
+    } else {
+        uint32_t c[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            c[i] = bf16x2_bits(__floats2bfloat162_rn(__double2float_rn(y[2 * i]), __double2float_rn(y[2 * i + 1])));
+        if (on) {
+            reinterpret_cast<uint4 *>(dst)[2 * lane] = make_uint4(c[0], c[1], c[2], c[3]);
+            reinterpret_cast<uint4 *>(dst)[2 * lane + 1] = make_uint4(c[4], c[5], c[6], c[7]);
         }
     }
 }
@@ -179,24 +222,29 @@ __device__ __forceinline__ __nv_bfloat162 rotate_bf16(float re, float im, float2
 }
 
 // Row r = (b, s): y = c * rsqrt(mean(c^2) + eps) * w (without norm_w, y = c),
-// k_pe times the position's (cos, sin), then the format's rounding.
-template <int F, typename T>
+// k_pe times the position's (cos, sin), then the format's rounding.  (Without a
+// norm nothing is rounded from 64 bits, and the registers around that call are free.)
+template <int F, typename T, bool norm>
 __global__ void __launch_bounds__(32 * kProWarps, kProBlocks) latent_prologue_kernel(const PrologueArgs a) {
     // the norm's weights, a lane's 32 at a pitch that keeps lanes off each
     // other's banks
     constexpr int kPitch = kVals + 4;
     __shared__ float4 w_sm[16 * kPitch / 4], w_flat[512 / 4];
     const int lane = threadIdx.x & 31, l16 = lane & 15;
-    const bool norm = a.norm_w != nullptr;
     static_assert(32 * kProWarps >= 512 / 4, "one load fills the weights");
+    bool far_out = false;          // weights with which products could leave fp32's range
     if (norm && threadIdx.x < a.dc / 4) {
         const float4 v = reinterpret_cast<const float4 *>(a.norm_w)[threadIdx.x];
         w_flat[threadIdx.x] = v;
         w_sm[(threadIdx.x / 8) * (kPitch / 4) + threadIdx.x % 8] = v;
+        const float top = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+        auto small = [](float x) { return x != 0.f && fabsf(x) < 0x1p-60f; };
+        far_out = top > 0x1p60f || small(v.x) || small(v.y) || small(v.z) || small(v.w);
     }
-    __syncthreads();
+    far_out = __syncthreads_or(far_out);
     const int64_t rb = latent_fmt_row_bytes(F, a.dc, a.dr);
     const float inv_dc = 1.f / (float)a.dc;
+    const double inv_dc64 = 1.0 / a.dc;
     const bool has_c = kVals * l16 < a.dc;
     // rotary pairs 2 l and 2 l + 1: elements 4 l .. 4 l + 3, or, when the
     // embedding is not interleaved, 2 l, 2 l + 1 and those dr/2 further on
@@ -239,39 +287,62 @@ __global__ void __launch_bounds__(32 * kProWarps, kProBlocks) latent_prologue_ke
 
         float rms = 1.f;
         bool doubt = false;
-        if (norm) {
-            const auto mean_square = [&](float eps) {      // of the half warp's row, plus eps
-                float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+        if constexpr (norm) {
+            // What fp32 may be off by, with u = 2^-24: the sum's chains of eight, two
+            // and four steps and the mean 16 u, so the root 8 u and 2 u of its own; a
+            // product u each.  bf16 values, where every one of a row's 512 is next to
+            // a border now and then, take the sum and the root in 64 bits.
+            if constexpr (F == DSA_BF16) {
+                double s0 = 0.0, s1 = 0.0;
 #pragma unroll
-                for (int e = 0; e < kVals / 2; e += 2) {
-                    s0 = __ffma2_rn(x[e], x[e], s0);
-                    s1 = __ffma2_rn(x[e + 1], x[e + 1], s1);
+                for (int e = 0; e < kVals / 2; e++) {
+                    s0 = fma((double)x[e].x, (double)x[e].x, s0);
+                    s1 = fma((double)x[e].y, (double)x[e].y, s1);
                 }
-                float ss = (s0.x + s0.y) + (s1.x + s1.y);
+                s0 += s1;
 #pragma unroll
-                for (int m = 8; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-                return fmaf(ss, inv_dc, eps);
-            };
-            float v = mean_square(a.eps);
-            doubt = !(v > 0x1p-80f && v < 0x1p80f);        // squares that fp32 cannot hold
-            if constexpr (F == DSA_FP8_LATENT) {
-                // such a row is taken times a power of two, which the norm takes
-                // out again (the other formats round it from 64-bit sums below)
-                if (__any_sync(0xffffffffu, doubt)) {
-                    const float k = !doubt ? 1.f : v < 1.f ? 0x1p90f : 0x1p-80f;
+                for (int m = 8; m > 0; m >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, m);
+                const double v = fma(s0, inv_dc64, (double)a.eps);
+                const float vf = (float)v;
+                doubt = far_out || !(vf > 0x1p-80f && vf < 0x1p80f);       // squares that fp32 cannot hold
+                const double r0 = (double)rsqrtf(vf);
+                rms = (float)fma(r0 * 0.5, fma(-v * r0, r0, 1.0), r0);     // a Newton step
+            } else {
+                const auto mean_square = [&](float eps) {  // of the half warp's row, plus eps
+                    float2 s0 = make_float2(0.f, 0.f), s1 = s0;
 #pragma unroll
-                    for (int e = 0; e < kVals / 2; e++) x[e] = __fmul2_rn(x[e], splat(k));
-                    v = mean_square(a.eps * k * k);
+                    for (int e = 0; e < kVals / 2; e += 2) {
+                        s0 = __ffma2_rn(x[e], x[e], s0);
+                        s1 = __ffma2_rn(x[e + 1], x[e + 1], s1);
+                    }
+                    float ss = (s0.x + s0.y) + (s1.x + s1.y);
+#pragma unroll
+                    for (int m = 8; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+                    return fmaf(ss, inv_dc, eps);
+                };
+                float v = mean_square(a.eps);
+                doubt = !(v > 0x1p-80f && v < 0x1p80f);    // squares that fp32 cannot hold
+                if constexpr (F == DSA_FP8_LATENT) {
+                    // such a row is taken times a power of two, which the norm takes
+                    // out again (4-bit rows are rounded from 64-bit sums below)
+                    if (__any_sync(0xffffffffu, doubt)) {
+                        const float k = !doubt ? 1.f : v < 1.f ? 0x1p90f : 0x1p-80f;
+#pragma unroll
+                        for (int e = 0; e < kVals / 2; e++) x[e] = __fmul2_rn(x[e], splat(k));
+                        v = mean_square(a.eps * k * k);
+                    }
+                } else {
+                    doubt |= far_out;
                 }
-            }
-            rms = rsqrtf(v);
-            if (rms != 0.f) rms = fmaf(rms * 0.5f, fmaf(-v * rms, rms, 1.f), rms);      // a Newton step: within a rounding or two
+                rms = rsqrtf(v);
+                if (rms != 0.f) rms = fmaf(rms * 0.5f, fmaf(-v * rms, rms, 1.f), rms);      // a Newton step: within a rounding or two
 #pragma unroll
-            for (int e = 0; e < kVals / 4; e++) {
-                const float4 wv = w_sm[l16 * (kPitch / 4) + e];
-                // the norm's factor comes later
-                x[2 * e] = __fmul2_rn(x[2 * e], make_float2(wv.x, wv.y));
-                x[2 * e + 1] = __fmul2_rn(x[2 * e + 1], make_float2(wv.z, wv.w));
+                for (int e = 0; e < kVals / 4; e++) {
+                    const float4 wv = w_sm[l16 * (kPitch / 4) + e];
+                    // the norm's factor comes later
+                    x[2 * e] = __fmul2_rn(x[2 * e], make_float2(wv.x, wv.y));
+                    x[2 * e + 1] = __fmul2_rn(x[2 * e + 1], make_float2(wv.z, wv.w));
+                }
             }
         }
         if constexpr (F == DSA_BF16) {
@@ -280,10 +351,13 @@ __global__ void __launch_bounds__(32 * kProWarps, kProBlocks) latent_prologue_ke
                 uint32_t c[4];
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
-                    const float2 y = __fmul2_rn(x[4 * i + e], splat(rms));
+                    const float4 wv = norm ? w_sm[l16 * (kPitch / 4) + 2 * i + e / 2] : make_float4(1.f, 1.f, 1.f, 1.f);
+                    // (weight times root stays in range whatever x is)
+                    const float2 y = __fmul2_rn(x[4 * i + e], __fmul2_rn(e & 1 ? make_float2(wv.z, wv.w) : make_float2(wv.x, wv.y), splat(rms)));
                     c[e] = bf16x2_bits(__floats2bfloat162_rn(y.x, y.y));
-                    // the part below bf16 within 4 of 2^16 units of the middle
-                    doubt |= ((__float_as_uint(y.x) + 0x8004u) & 0xFFFFu) < 8u || ((__float_as_uint(y.y) + 0x8004u) & 0xFFFFu) < 8u;
+                    // three roundings, less than three of the 2^16 units below bf16: in
+                    // doubt within four units of the middle
+                    doubt |= ((__float_as_uint(y.x) + 0x8004u) & 0xFFFFu) <= 8u || ((__float_as_uint(y.y) + 0x8004u) & 0xFFFFu) <= 8u;
                 }
                 if (on && has_c) reinterpret_cast<uint4 *>(dst)[4 * l16 + i] = make_uint4(c[0], c[1], c[2], c[3]);
             }
@@ -326,9 +400,11 @@ __global__ void __launch_bounds__(32 * kProWarps, kProBlocks) latent_prologue_ke
                 const float st = div_rn_by(max_nan(amax * rms, 1e-4f), 7.0f, 1.0f / 7.0f);
                 const __nv_bfloat16 sb = __float2bfloat16_rn(st);
                 const float sc = __bfloat162float(sb), rs = __frcp_rn(sc);
-                if (norm) {
-                    // in doubt: a quotient (seven at most, a few roundings off)
-                    // within 2^-19 of a border, a scale within 2 of 2^16 units
+                if constexpr (norm) {
+                    // in doubt: a quotient, off by 14 u of itself (weight, root, the
+                    // scale's reciprocal, two products), which is 2^-17.3 at seven,
+                    // within 2^-17 of a border; a scale, off by 13 u or fewer than 13
+                    // of the 2^16 units below bf16, within 16 units of the middle
                     const float2 k = splat(rms * rs);
                     float far = 0.f;
 #pragma unroll
@@ -339,7 +415,7 @@ __global__ void __launch_bounds__(32 * kProWarps, kProBlocks) latent_prologue_ke
                         const float2 d = __ffma2_rn(q, splat(-1.f), n);
                         far = fmaxf(far, fmaxf(fabsf(d.x), fabsf(d.y)));
                     }
-                    doubt |= far > 0.5f - 0x1p-19f || ((__float_as_uint(st) + 0x8002u) & 0xFFFFu) < 4u;
+                    doubt |= far > 0.5f - 0x1p-17f || ((__float_as_uint(st) + 0x8010u) & 0xFFFFu) <= 32u;
                 } else {
                     const float2 rs2 = splat(rs), ns2 = splat(-sc);
 #pragma unroll
@@ -354,7 +430,7 @@ __global__ void __launch_bounds__(32 * kProWarps, kProBlocks) latent_prologue_ke
                 }
             }
         }
-        if (F != DSA_FP8_LATENT && norm) {
+        if constexpr (F != DSA_FP8_LATENT && norm) {
             const uint32_t rows = __ballot_sync(0xffffffffu, doubt && on && has_c);
             if (rows) {
                 __syncwarp();                              // the fp32 result's stores come first
@@ -486,16 +562,16 @@ unsigned warp_grid(int64_t rows, int cap) {
     return (unsigned)(blocks < most ? blocks : most);
 }
 
-template <typename T>
+template <typename T, bool norm>
 void launch_prologue(dsa_dtype fmt, const PrologueArgs &a, cudaStream_t st) {
     const int64_t blocks = (a.rows + 2 * kProWarps - 1) / (2 * kProWarps);
     const unsigned grid = (unsigned)std::min<int64_t>(blocks, (int64_t)num_sms() * kProBlocks);   // each warp strides on
     if (fmt == DSA_BF16)
-        latent_prologue_kernel<DSA_BF16, T><<<grid, 32 * kProWarps, 0, st>>>(a);
+        latent_prologue_kernel<DSA_BF16, T, norm><<<grid, 32 * kProWarps, 0, st>>>(a);
     else if (fmt == DSA_FP8_LATENT)
-        latent_prologue_kernel<DSA_FP8_LATENT, T><<<grid, 32 * kProWarps, 0, st>>>(a);
+        latent_prologue_kernel<DSA_FP8_LATENT, T, norm><<<grid, 32 * kProWarps, 0, st>>>(a);
     else
-        latent_prologue_kernel<DSA_Q4_LATENT, T><<<grid, 32 * kProWarps, 0, st>>>(a);
+        latent_prologue_kernel<DSA_Q4_LATENT, T, norm><<<grid, 32 * kProWarps, 0, st>>>(a);
 }
 
 template <int F, typename T>
@@ -566,9 +642,9 @@ extern "C" dsa_status dsa_latent_prologue(const void *kv, dsa_dtype x_dtype, int
     a.dr = dr;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (x_dtype == DSA_BF16)
-        dsa::launch_prologue<__nv_bfloat16>(cache_dt, a, st);
+        norm_w ? dsa::launch_prologue<__nv_bfloat16, true>(cache_dt, a, st) : dsa::launch_prologue<__nv_bfloat16, false>(cache_dt, a, st);
     else
-        dsa::launch_prologue<float>(cache_dt, a, st);
+        norm_w ? dsa::launch_prologue<float, true>(cache_dt, a, st) : dsa::launch_prologue<float, false>(cache_dt, a, st);
     return dsa::launch_status();
 }
 
