@@ -446,7 +446,8 @@ dsa_status dsa_block_mla_attn(const void *q, const void *kv_cache, dsa_dtype cac
  * dt = DSA_FP8_LATENT: kv_cache is the FP8 latent cache [B, t_max,
  * dsa_latent_row_bytes(dc, dr)] (16-byte aligned), attended as
  * dsa_sparse_mla_attn_fp8 does; q_mla and out are bf16.  dt = DSA_Q4_LATENT:
- * likewise the 4-bit latent cache, attended as dsa_sparse_mla_attn_q4 does.
+ * likewise the 4-bit latent cache, attended as dsa_sparse_mla_attn_q4 does, with
+ * its limits (K up to 2^30 - 1, else DSA_ERR_UNSUPPORTED).
  */
 size_t dsa_decode_step_workspace_size(int B, int H, int D, int64_t T, int index_topk, int Hq,
                                       int dc, int dr, dsa_dtype dt);

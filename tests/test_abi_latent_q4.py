@@ -186,3 +186,23 @@ def test_block_keys_refuse_blocks_past_their_counters(dsa):
         assert keys(dsa._lib, m=m, t_max=1 << 32, S=1 << 32) == UNSUPPORTED
         assert keys(dsa._lib, m=m, t_max=1 << 32, S=1, D=64) == UNSUPPORTED
     assert keys(dsa._lib, m=1 << 20, k=NULL, S=(1 << 20) - 1, t_max=1 << 20) == OK      # finishes no block
+
+
+def test_decode_step_refuses_selections_past_the_attentions(dsa):
+    """2^30 rows and more, which dsa_sparse_mla_attn_q4 refuses too (its slot numbers are 32-bit)."""
+    L = dsa._lib
+    T = (1 << 31) - 1
+
+    def size(T, topk, dt=Q4):
+        return L.dsa_decode_step_workspace_size(1, 1, 64, T, topk, 1, 128, 0, dt)
+
+    def call(T, topk):
+        return L.dsa_decode_step(FAKE, FAKE, FAKE, FAKE, FAKE, T, FAKE, FAKE, 1, 1, 64, 1, 128, 0, T, topk, 0.1,
+                                 0.1, Q4, FAKE, FAKE, NULL, FAKE, 0, NULL)
+    for K in (1 << 30, T - 100, T):
+        assert size(T, K) == 0 and call(T, K) == UNSUPPORTED
+        assert L.dsa_decode_step_noalloc(FAKE, FAKE, FAKE, FAKE, FAKE, T, FAKE, FAKE, 1, 1, 64, 1, 128, 0, T, K,
+                                         0.1, 0.1, Q4, FAKE, FAKE, NULL, NULL) in (UNSUPPORTED, 3)   # (3: no device)
+    # min(index_topk, T) counts, and the largest selection is taken (its scores alone are T floats)
+    assert size(T, (1 << 30) - 1) >= 4 * T and call(T, (1 << 30) - 1) == WORKSPACE
+    assert size(1000, T) >= 4000 and call(1000, T) == WORKSPACE

@@ -12,6 +12,12 @@
 namespace dsa {
 namespace {
 
+// The attention over 4-bit rows takes selections of fewer than 2^30 rows (as
+// dsa_sparse_mla_attn_q4 does).
+bool selection_ok(dsa_dtype dt, int64_t T, int index_topk) {
+    return dt != DSA_Q4_LATENT || T < 1 << 30 || index_topk < 1 << 30;
+}
+
 struct DecodeWs {
     float *scores;     // [B,T]
     uint32_t *hist;    // [B][chunks][kHistBins]: each scorer CTA's scores counted by their
@@ -51,6 +57,7 @@ DecodeWs carve(void *base, int B, int H, int D, int64_t T, int index_topk, int H
 extern "C" size_t dsa_decode_step_workspace_size(int B, int H, int D, int64_t T, int index_topk,
                                                  int Hq, int dc, int dr, dsa_dtype dt) {
     if (B <= 0 || H <= 0 || T <= 0 || index_topk <= 0) return 0;
+    if (!dsa::selection_ok(dt, T, index_topk)) return 0;   // (the call refuses it)
     return dsa::carve(nullptr, B, H, D, T, index_topk, Hq, dc, dr, dt).total;
 }
 
@@ -72,6 +79,7 @@ extern "C" dsa_status dsa_decode_step(const float *q_idx, const float *w, const 
     if ((dt == DSA_FP8_LATENT || dt == DSA_Q4_LATENT) && !dsa::latent_fp8_shape_ok(dc, dr))
         return DSA_ERR_UNSUPPORTED;
     if (dt == DSA_Q4_LATENT && Hq > 1024) return DSA_ERR_UNSUPPORTED;
+    if (!dsa::selection_ok(dt, T, index_topk)) return DSA_ERR_UNSUPPORTED;
     if (B == 0) return DSA_OK;
     if (!q_idx || !w || !k_new || !k_cache || !k_scale || !kv_cache || !q_mla || !idx || !out)
         return DSA_ERR_INVALID_ARG;

@@ -707,6 +707,7 @@ struct Plan {
     size_t o_bytes, total;
 };
 
+// (slots: up to 2^30, which leaves the kernel's slot numbers room in 32 bits)
 Plan make_plan(int64_t rows, int Hq, int dc, int slots) {
     Plan p;
     // the MMA's N: a head count that fits 16 or 32 columns takes that many
