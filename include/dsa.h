@@ -374,8 +374,8 @@ dsa_status dsa_latent_read(const void *cache, dsa_dtype cache_dt, int64_t t_max,
  * cache kv_q4 [B, t_max, dsa_latent_q4_row_bytes(dc, dr)], 16-byte aligned.
  *   q    [B,S,Hq,dc+dr] bf16 (16-byte aligned), idx [B,S,k] int32 (-1 = empty)
  *   out  [B,S,Hq,dc] bf16 (16-byte aligned), lse [B,S,Hq] fp32 or NULL
- * Hq up to 1024, k up to 2^30 - 1; shapes as dsa_latent_quant.  Each query row's selection is
- * masked as in dsa_sparse_mla_attn (-1 and indices > start_pos + s are skipped;
+ * Hq up to 1024, k up to 2^30 - 1, B*S*Hq up to 2^31 - 1 (else
+ * DSA_ERR_UNSUPPORTED); shapes as dsa_latent_quant.  Each query row's selection is masked as in dsa_sparse_mla_attn (-1 and indices > start_pos + s are skipped;
  * a row with nothing left gives out = 0, lse = -inf).
  * Workspace: dsa_sparse_mla_attn_q4_workspace_size bytes (16-byte aligned).
  */

@@ -206,3 +206,12 @@ def test_decode_step_refuses_selections_past_the_attentions(dsa):
     # min(index_topk, T) counts, and the largest selection is taken (its scores alone are T floats)
     assert size(T, (1 << 30) - 1) >= 4 * T and call(T, (1 << 30) - 1) == WORKSPACE
     assert size(1000, T) >= 4000 and call(1000, T) == WORKSPACE
+
+
+@pytest.mark.parametrize("blocks", [False, True])
+def test_selections_of_more_entries_than_31_bits_are_taken(dsa, blocks):
+    """2^20 query rows of 2048 entries: no documented limit refuses them (the misaligned query
+    is what this call stops at)."""
+    kw = dict(S=1 << 20, t_max=1 << 21, sp=0, Hq=16, k=2048, q=ODD)
+    assert attn(dsa, blocks, **kw, **(dict(m=16) if blocks else {})) == INVALID
+    assert attn(dsa, blocks, **{**kw, "Hq": 1024, "S": 1 << 21}) == UNSUPPORTED       # B * S * Hq = 2^31

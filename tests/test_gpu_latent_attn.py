@@ -216,6 +216,25 @@ def test_offsets_beyond_32_bits(dsa):
     assert not bs[:, :-2].any()
 
 
+def test_selections_of_more_entries_than_31_bits(dsa):
+    """2^20 query rows of 2049 slots, a few of them filled, in the last ones too: the lists'
+    offsets pass 2^31 entries."""
+    S, k, dc, dr, sp = 1 << 20, 2049, 128, 0, 5000
+    small, rows = make_cache(dsa, 1, 4096, R.Q4, dc, dr, seed=2)
+    cache = torch.zeros(1, sp + S, small.shape[-1], dtype=torch.uint8, device="cuda")
+    cache[:, :4096] = small
+    q = torch.randn(1, S, 2, dc, dtype=torch.bfloat16, device="cuda")
+    idx = torch.full((1, S, k), -1, dtype=torch.int32, device="cuda")
+    s = torch.arange(S, device="cuda", dtype=torch.int32)
+    for j, slot in enumerate((0, 1, 700, 2048)):
+        idx[0, :, slot] = (s * (j + 3) + 1000 * j) % 1000 + 1000 * j
+    out, lse = run_attn(dsa, q, cache, R.Q4, idx, 0, sp, 0.1, dc)
+    for at in (0, (1 << 31) // k - 1, (1 << 31) // k, S - 3):
+        check(q[:, at:at + 3], rows, idx[:, at:at + 3], 0, sp + at, 0.1, dc, out[:, at:at + 3], lse[:, at:at + 3])
+    del idx, cache, q, out, lse
+    torch.cuda.empty_cache()
+
+
 def test_empty_rows(dsa):
     B, S, Hq, dc, dr, t_max, k = 3, 2, 128, 512, 64, 300, 300
     q = make_q(B, S, Hq, dc + dr, 1)

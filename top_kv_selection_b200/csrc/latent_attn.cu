@@ -828,7 +828,7 @@ dsa_status check_attn(const void *q, const void *kv, int64_t t_max, const int32_
     if (Hq > 1024 || block > 1 << 20) return DSA_ERR_UNSUPPORTED;
     if (B == 0 || S == 0 || Hq == 0) return DSA_OK;
     if (t_max > INT32_MAX || t_max < S || start_pos > t_max - S) return DSA_ERR_INVALID_ARG;
-    if ((int64_t)B * S > INT32_MAX || (int64_t)B * S * n_sel > INT32_MAX || (int64_t)B * S * Hq > INT32_MAX ||
+    if ((int64_t)B * S > INT32_MAX || (int64_t)B * S * Hq > INT32_MAX ||
         ((int64_t)n_sel + 1) * (block ? block : 1) > 1 << 30)
         return DSA_ERR_UNSUPPORTED;
     if (!q || !kv || (!sel && n_sel > 0) || !out) return DSA_ERR_INVALID_ARG;
