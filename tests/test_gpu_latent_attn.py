@@ -330,6 +330,63 @@ def test_first_tiles_with_nothing_selected_and_logits_far_from_zero(dsa, shift):
                   out[:, s:s + 1], lse[:, s:s + 1])
 
 
+@pytest.mark.parametrize("power", [0, 10, 60, 110, 124])
+@pytest.mark.parametrize("sign", [-1, 1])
+@pytest.mark.parametrize("S", [1, 200])                 # one tile a CTA, and every tile in one CTA
+def test_equal_logits_as_far_from_zero_as_fp32_goes(dsa, S, sign, power):
+    """Every selected row has the same logit, sign * 7 * 2^power, exactly (one nonzero column of
+    q, a power of two, against a 4-bit value without rounding), after 128-slot tiles that hold
+    no valid slot: the weights are equal whatever the logit is, the output is the mean.  Sums of
+    up to 512 fp32 terms and the two roundings of the weights and the output."""
+    dc, dr, t_max, k, n = 512, 64, 700, 512, 212
+    kv = torch.randn(1, t_max, dc + dr, generator=torch.Generator().manual_seed(power))
+    kv[..., :32] = 0
+    kv[..., 5] = sign * 7 * 2.0 ** (power // 2)
+    raw = torch.zeros(1, t_max, 416, dtype=torch.uint8, device="cuda")
+    dsa.dsa_latent_prologue(kv.cuda(), None, 0.0, None, False, 0, raw, R.Q4, dc)
+    rows = R.decode_rows(raw.cpu().numpy(), R.Q4, dc, dr)
+    assert np.all(rows[..., 5] == sign * 7 * 2.0 ** (power // 2))
+    q = torch.zeros(1, S, 24, dc + dr, dtype=torch.bfloat16, device="cuda")
+    q[..., 5] = 2.0 ** (power - power // 2)
+    idx = torch.full((1, S, k), -1, dtype=torch.int32)
+    idx[:, :, k - n:] = torch.randperm(t_max - S, generator=torch.Generator().manual_seed(1))[:n].sort().values.int()
+    out, lse = run_attn(dsa, q, raw, R.Q4, idx.cuda(), 0, t_max - S, 1.0, dc)
+    sel = rows[0, idx[0, 0, k - n:].numpy()][:, 32:dc]
+    got, want = out[..., 32:].double().cpu().numpy(), sel.mean(0)
+    assert np.all(np.abs(got - want) <= np.abs(want) * 2.0 ** -8 + np.abs(sel).mean(0) * (512 * 2.0 ** -24))
+    z = sign * 7 * 2.0 ** power
+    assert np.all(np.abs(lse.double().cpu().numpy() - (z + np.log(n))) <= abs(z) * 2.0 ** -22 + 2.0 ** -18)
+
+
+@pytest.mark.parametrize("sm", [0.0, 1e-30, 1e30, -1e30])
+@pytest.mark.parametrize("S", [1, 200])
+def test_scales_far_from_one(dsa, S, sm):
+    """A scale of zero (or nothing) weighs all selected rows alike; a huge one leaves the row with
+    the largest logit, or the smallest where it is negative (whole numbers, so that logits are
+    exact and far apart once scaled), its share the other rows with that logit have too."""
+    dc, dr, t_max, k = 256, 8, 700, 400
+    g = torch.Generator().manual_seed(4)
+    kv = torch.randint(-7, 8, (1, t_max, dc + dr), generator=g).float()
+    kv[..., 0:dc:32] = 7                                 # (a 4-bit step of one)
+    raw = torch.zeros(1, t_max, R.row_bytes(R.Q4, dc, dr), dtype=torch.uint8, device="cuda")
+    dsa.dsa_latent_prologue(kv.cuda(), None, 0.0, None, False, 0, raw, R.Q4, dc)
+    rows = R.decode_rows(raw.cpu().numpy(), R.Q4, dc, dr)
+    assert np.array_equal(rows, kv.double().numpy())
+    q = torch.randint(-3, 4, (1, S, 20, dc + dr), generator=g).to(torch.bfloat16)
+    idx = torch.full((1, S, k), -1, dtype=torch.int32)
+    idx[:, :, 140:] = torch.randperm(t_max - S, generator=g)[:k - 140].int()
+    out, lse = run_attn(dsa, q.cuda(), raw, R.Q4, idx.cuda(), 0, t_max - S, sm, dc)
+    z = np.einsum("shd,td->sht", q[0].double().numpy(), rows[0, idx[0, 0, 140:].numpy()])
+    p = np.ones_like(z) if abs(sm) < 1 else (z == (z.max(-1, keepdims=True) if sm > 0 else z.min(-1, keepdims=True)))
+    p = p / p.sum(-1, keepdims=True)
+    sel = rows[0, idx[0, 0, 140:].numpy(), :dc]
+    got, want = out[0].double().cpu().numpy(), p @ sel
+    # the weights are 1 or 0: the rounding of the output, and the fp32 sums and quotient
+    assert np.all(np.abs(got - want) <= np.abs(want) * 2.0 ** -8 + (p @ np.abs(sel)) * (400 * 2.0 ** -24))
+    if abs(sm) < 1:
+        assert np.all(np.abs(lse[0].double().cpu().numpy() - np.log(k - 140)) <= 2.0 ** -18)
+
+
 @pytest.mark.parametrize("S", [1, 200])                 # split over CTAs, and one CTA a row
 def test_nan_stays_where_it_belongs(dsa, S):
     """A NaN in one head's query makes that head NaN, in a selected row every head of that

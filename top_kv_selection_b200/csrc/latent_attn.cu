@@ -47,6 +47,9 @@
 // a second kernel merges (fp16 ones with a power of two per 32 columns halved
 // the bytes, but the maxima they need cost more than the bytes: 24.9 against
 // 21.2 us at eight rows of 2048 slots).
+#include <cfloat>
+#include <cmath>
+
 #include "latent_rows.cuh"
 #include "tc_ptx.cuh"
 
@@ -60,9 +63,11 @@ constexpr int kThreads = kWork + 32;
 constexpr int kMaxHeads = 64;                   // heads per CTA
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// stands for a head's reference until it has one: every finite logit passes it
-// by more than the slack, and 2^(-inf - kUnseen) is 0
-constexpr float kUnseen = -1e30f;
+// stands for a head's reference until it has one: the lowest number, so that every
+// finite logit above it passes it by more than the slack (kLeastScale times 2^128 is
+// 32); -inf - kUnseen is -inf
+constexpr float kUnseen = -FLT_MAX;
+constexpr float kLeastScale = 0x1p-123f;
 constexpr float kSlack = 8.f;                   // how far (log2) a logit may pass the reference
 
 struct AttnArgs {
@@ -77,14 +82,15 @@ struct AttnArgs {
     int n_sel, block, slots;    // block = 0: the list holds positions
     int S, Hq, dc, dr;
     int groups, splits, split_slots;
-    float scale_log2;           // sm_scale * log2(e)
+    float scale;                // |sm_scale| * log2(e), at least kLeastScale
+    float sign;                 // of sm_scale
     int *err;
 };
 
 // Control block behind the tiles and the query.
 struct alignas(16) Control {
     float red[4][kMaxHeads];    // per TMEM lane quarter: maxima, later sums
-    float ref[kMaxHeads];       // the heads' references (-inf: no logit seen)
+    float ref[kMaxHeads];       // the heads' references, of sign * q . c (-inf: no logit seen)
     float sub[kMaxHeads];       // what is subtracted: the reference, or kUnseen
     float fac[kMaxHeads];       // rescaling of this tile; at the end 1 / sum
     uint64_t full[5];           // chunk pair m (4: the rotary chunk) is in shared memory
@@ -448,7 +454,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
                     uint32_t pk[4];
 #pragma unroll
                     for (int e = 0; e < 8; e++) {
-                        const float z = fmaf(__uint_as_float(v[x + e]), a.scale_log2, -sub[e]);
+                        // (the difference before the scale: it is 0 at the maximum
+                        // however far that is from zero)
+                        const float z = fmaf(__uint_as_float(v[x + e]), a.sign, -sub[e]) * a.scale;
                         over |= z > kSlack;
                         p[x + e] = valid ? ex2(z) : 0.f;
                     }
@@ -469,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
                     ld_cols(scol, v);
                     tc::tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < kCols; e++) p[e] = valid ? __uint_as_float(v[e]) * a.scale_log2 : -INFINITY;
+                    for (int e = 0; e < kCols; e++) p[e] = valid ? __uint_as_float(v[e]) * a.sign : -INFINITY;
                     const int e = reduce_lanes(p, [](float x, float y) { return fmaxf(x, y); });
                     if ((lane & (32 / kCols - 1)) == 0) ctl.red[q4][c * kCols + e] = p[0];
                 }
@@ -478,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
                     const float old = ctl.ref[t];
                     const float m = fmaxf(fmaxf(fmaxf(ctl.red[0][t], ctl.red[1][t]),
                                                 fmaxf(ctl.red[2][t], ctl.red[3][t])), old);
-                    ctl.fac[t] = old == m ? 1.f : ex2(old - m);
+                    ctl.fac[t] = old == m ? 1.f : ex2((old - m) * a.scale);
                     ctl.ref[t] = m;
                     ctl.sub[t] = m == -INFINITY ? kUnseen : m;
                 }
@@ -531,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
                 // (a NaN sum makes the reference NaN, so that the merge keeps it)
                 a.part_ml[(int64_t)blockIdx.x * NH + t] = make_float2(l == 0.f ? -INFINITY : l != l ? l : ctl.ref[t], l);
             else if (a.lse)
-                a.lse[row * a.Hq + h0 + t] = l == 0.f ? -INFINITY : (ctl.ref[t] + log2f(l)) * kLn2;
+                a.lse[row * a.Hq + h0 + t] = l == 0.f ? -INFINITY : fmaf(ctl.ref[t], a.scale, log2f(l)) * kLn2;
         }
     } else {
         // ------------------------------------------------------------- MMA
@@ -652,12 +660,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attn_kernel(const AttnArgs
 
 // Merges a row's splits: block = one head of one row, thread = four output
 // columns.
-//   M = max_s ref_s,  out = sum_s 2^(ref_s - M) O_s / sum_s 2^(ref_s - M) l_s
+//   M = max_s ref_s,  w_s = 2^(scale (ref_s - M)),  out = sum_s w_s O_s / sum_s w_s l_s
 // Every warp works the splits' weights out for itself (lane = split), so that
 // the partials' loads depend on two loads and no barrier; eight are in flight.
 __global__ void __launch_bounds__(128)
 latent_combine_kernel(const float *part_o, const float2 *part_ml, int splits, int groups, int nh, int Hq, int dc,
-                      __nv_bfloat16 *out, float *lse) {
+                      float scale, __nv_bfloat16 *out, float *lse) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t row = blockIdx.x / (unsigned)Hq;
@@ -672,9 +680,9 @@ latent_combine_kernel(const float *part_o, const float2 *part_ml, int splits, in
     float L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int s0 = 0; s0 < splits; s0 += 32) {
-        // an empty share has l = 0 and wrote no partial: weight 0, not read
+        // an empty share has l = 0 and a partial of zeros: weight 0, not read
         const float2 v = s0 + lane < splits ? ml[(int64_t)(s0 + lane) * nh] : make_float2(-INFINITY, 0.f);
-        const float w = v.y == 0.f ? 0.f : v.x == M ? 1.f : ex2(v.x - M);
+        const float w = v.y == 0.f ? 0.f : v.x == M ? 1.f : ex2((v.x - M) * scale);
         const uint32_t live = __ballot_sync(0xffffffffu, v.y != 0.f);
         L += warp_sum(w == 0.f ? 0.f : w * v.y);
         const int n = splits - s0 < 32 ? splits - s0 : 32;
@@ -698,7 +706,7 @@ latent_combine_kernel(const float *part_o, const float2 *part_ml, int splits, in
     w2.x = bf16x2_bits(__floats2bfloat162_rn(acc.x * inv, acc.y * inv));
     w2.y = bf16x2_bits(__floats2bfloat162_rn(acc.z * inv, acc.w * inv));
     reinterpret_cast<uint2 *>(out + (row * Hq + head) * dc)[threadIdx.x] = w2;
-    if (threadIdx.x == 0 && lse) lse[row * Hq + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+    if (threadIdx.x == 0 && lse) lse[row * Hq + head] = L == 0.f ? -INFINITY : fmaf(M, scale, log2f(L)) * kLn2;
 }
 
 // How a call is cut: heads per CTA, head groups, splits of each row's slots.
@@ -793,7 +801,9 @@ dsa_status launch_latent_attn(const void *q, const void *kv, dsa_dtype fmt, int6
     a.groups = p.groups;
     a.splits = p.splits;
     a.split_slots = p.split_slots;
-    a.scale_log2 = sm_scale * kLog2e;
+    a.sign = copysignf(1.f, sm_scale);
+    a.scale = fabsf(sm_scale) * kLog2e;
+    if (a.scale < kLeastScale) a.scale = kLeastScale;
     a.err = device_error_word();
     const unsigned grid = (unsigned)(rows * p.groups * p.splits);
     const dsa_status s = fmt == DSA_BF16         ? launch_heads<DSA_BF16>(a, p.nh, grid, st)
@@ -810,7 +820,7 @@ dsa_status launch_latent_attn(const void *q, const void *kv, dsa_dtype fmt, int6
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, latent_combine_kernel, (const float *)a.part_o, (const float2 *)a.part_ml,
-                           p.splits, p.groups, p.nh, Hq, dc, a.out, lse) != cudaSuccess)
+                           p.splits, p.groups, p.nh, Hq, dc, a.scale, a.out, lse) != cudaSuccess)
         return DSA_ERR_CUDA;
     return launch_status();
 }
