@@ -215,3 +215,16 @@ def test_selections_of_more_entries_than_31_bits_are_taken(dsa, blocks):
     kw = dict(S=1 << 20, t_max=1 << 21, sp=0, Hq=16, k=2048, q=ODD)
     assert attn(dsa, blocks, **kw, **(dict(m=16) if blocks else {})) == INVALID
     assert attn(dsa, blocks, **{**kw, "Hq": 1024, "S": 1 << 21}) == UNSUPPORTED       # B * S * Hq = 2^31
+
+
+def test_binding_refuses_other_types_than_bf16_over_the_4_bit_cache(dsa):
+    """The kernel reads q_mla and writes out as bf16 whatever the tensors hold."""
+    import torch
+    cache = torch.zeros(1, 4, 416, dtype=torch.uint8)
+    q, out = torch.zeros(1, 2, 576, dtype=torch.bfloat16), torch.zeros(1, 2, 512, dtype=torch.bfloat16)
+    assert dsa._kv_dtype(cache, q, out, 512) == Q4
+    for bad in ((q.float(), out), (q, out.float()), (q.half(), out)):
+        with pytest.raises(ValueError):
+            dsa._kv_dtype(cache, *bad, 512)
+    assert dsa._kv_dtype(torch.zeros(1, 4, 656, dtype=torch.uint8), q, out, 512) == FP8
+    assert dsa._kv_dtype(q, q, out, 512) == BF16

@@ -134,13 +134,17 @@ def _dtype(t: torch.Tensor) -> int:
     raise ValueError(f"unsupported dtype {t.dtype}")
 
 
-def _kv_dtype(kv_cache: torch.Tensor, q_mla: torch.Tensor, dc: int) -> int:
+def _kv_dtype(kv_cache: torch.Tensor, q_mla: torch.Tensor, out: torch.Tensor, dc: int) -> int:
     """The decode step's cache type: uint8 rows are the 4-bit latent cache when they
     have its width, else the FP8 latent cache (no shape has equal widths)."""
     if kv_cache.dtype != torch.uint8:
         return _dtype(q_mla)
     q4 = _lib.dsa_latent_q4_row_bytes(dc, q_mla.shape[-1] - dc)
-    return DSA_Q4_LATENT if kv_cache.shape[-1] == q4 else DSA_FP8_LATENT
+    if kv_cache.shape[-1] != q4:
+        return DSA_FP8_LATENT
+    if q_mla.dtype != torch.bfloat16 or out.dtype != torch.bfloat16:
+        raise ValueError("over the 4-bit latent cache q_mla and out must be bf16")
+    return DSA_Q4_LATENT
 
 
 _ROW_BYTES = {}
@@ -484,7 +488,7 @@ def dsa_decode_step(q_idx: torch.Tensor, w: torch.Tensor, k_new: torch.Tensor,
     _check("dsa_decode_step", _lib.dsa_decode_step(
         _ptr(q_idx), _ptr(w), _ptr(k_new), _ptr(k_cache), _ptr(k_scale), t_max, _ptr(kv_cache),
         _ptr(q_mla), B, H, D, Hq, dc, dqk - dc, T, index_topk, softmax_scale, sm_scale,
-        _kv_dtype(kv_cache, q_mla, dc), _ptr(idx), _ptr(out), _ptr(lse), _ptr(workspace),
+        _kv_dtype(kv_cache, q_mla, out, dc), _ptr(idx), _ptr(out), _ptr(lse), _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
@@ -503,4 +507,4 @@ def dsa_decode_step_noalloc(q_idx: torch.Tensor, w: torch.Tensor, k_new: torch.T
     _check("dsa_decode_step_noalloc", _lib.dsa_decode_step_noalloc(
         _ptr(q_idx), _ptr(w), _ptr(k_new), _ptr(k_cache), _ptr(k_scale), t_max, _ptr(kv_cache),
         _ptr(q_mla), B, H, D, Hq, dc, dqk - dc, T, index_topk, softmax_scale, sm_scale,
-        _kv_dtype(kv_cache, q_mla, dc), _ptr(idx), _ptr(out), _ptr(lse), _stream(stream)))
+        _kv_dtype(kv_cache, q_mla, out, dc), _ptr(idx), _ptr(out), _ptr(lse), _stream(stream)))
