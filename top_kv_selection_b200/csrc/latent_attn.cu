@@ -41,8 +41,8 @@
 //     rounded to bf16 as MMA operands (the sums take them unrounded).
 // Shared memory bounds the walk: a 128 x 64 x 16 MMA reads 6 KB in its 49
 // cycles, and the decoded tile is written beside it: 570 KB a tile, 2.3 of the
-// 3.8 us that one takes.  1024 queries of 2048 slots and 128 heads take 948 us
-// (616 TFLOP/s) over 4-bit rows, 8 queries 21 us.
+// 3.8 us that one takes.  1024 queries of 2048 slots and 128 heads take 945 us
+// (618 TFLOP/s) over 4-bit rows, 8 queries 20.5 us.
 // Splits of a row (when there are fewer rows than SMs) leave fp32 partials that
 // a second kernel merges (fp16 ones with a power of two per 32 columns halved
 // the bytes, but the maxima they need cost more than the bytes: 24.9 against

