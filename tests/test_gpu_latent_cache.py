@@ -242,6 +242,37 @@ def test_append_of_groups_next_to_a_border_of_their_scale(dsa, dc):
         assert np.all(same | near_half(quot))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_append_of_values_next_to_a_border_of_bf16(dsa, dtype):
+    """Every value of a normed row within six fp32 units of the middle between two bf16 numbers
+    (by its weight; by itself too where the row is fp32), rows of one magnitude: the stored
+    number is the exact value's."""
+    dc, rows = 512, 1500
+    g = np.random.default_rng(7)
+    for it in range(8):
+        x = torch.from_numpy((1 + 0.02 * g.random((rows, dc))) * g.choice([-1.0, 1.0], (rows, dc)) * g.uniform(0.5, 2, (rows, 1)))
+        x = x.to(dtype)
+        w = (1 + 0.3 * g.random(dc)).astype(np.float32)
+        def middle(y):
+            m, e = np.frexp(np.abs(y))
+            return np.ldexp((np.floor(m * 256) + 0.5) / 256, e) * (1 + g.uniform(-6, 6, y.shape) * 2.0 ** -23 / (2 * m))
+        for _ in range(4):
+            xd = x.double().numpy()
+            r = 1 / np.sqrt((xd * xd).mean(-1, keepdims=True) + 1e-6)
+            y = xd * r * w
+            if dtype == torch.float32:
+                x = torch.from_numpy(xd * middle(y) / np.abs(y)).to(dtype)
+            else:                                        # (each dim's weight by one of the rows)
+                at = g.integers(0, rows, dc), np.arange(dc)
+                w = (w * middle(y[at]) / np.abs(y[at])).astype(np.float32)
+        cache = new_cache(1, rows, R.BF16, dc, 0)
+        dsa.dsa_latent_prologue(x[None].contiguous().cuda(), torch.from_numpy(w).cuda(), 1e-6, None, False, 0, cache,
+                                R.BF16, dc)
+        y = R.prologue(x.double().numpy(), w.astype(np.float64), np.float64(np.float32(1e-6)), None, False, dc)
+        got = R.decode_rows(to_bytes(cache)[0], R.BF16, dc, 0)
+        assert np.array_equal(got, R.bf16(y.astype(np.float32))), int((got != R.bf16(y.astype(np.float32))).sum())
+
+
 @pytest.mark.parametrize("fmt", [R.BF16, R.Q4])
 def test_append_of_values_and_weights_far_apart(dsa, fmt):
     """Small values beside ordinary ones under weights far from one: no product on the way to
