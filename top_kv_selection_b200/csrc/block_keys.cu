@@ -9,7 +9,8 @@
 // A warp owns a block: one 16-byte load gives a lane 16 dims of a token, so
 // D / 16 lanes cover a token and a warp 512 / D tokens per load.  Each lane
 // sums its dims over its tokens in fp32 (packed pairs, up to sixteen tokens'
-// loads in flight); the lanes of a token group then trade halves until each
+// loads in flight, chains of sixteen and a chain of their sums, which is kept in
+// shared memory); the lanes of a token group then trade halves until each
 // holds the sums of D / 32 dims, in a fixed order.
 //
 // An fp32 sum's error goes by its terms and not by what is left of them when
@@ -17,10 +18,11 @@
 // alone, and takes dims whose code that leaves in doubt again in 64 bits: at 64
 // random tokens a block, about one dim in every third block.  Where the bound
 // passes 2^-14 of the largest dim, the scale's dim is among them.  138 MB of
-// keys in blocks of 64 tokens take 30.2 us, in blocks of 128 29.3, of 16 43.5,
-// of 2048 230 (there all blocks are summed twice); sums in 64 bits throughout
-// (two more integer instructions a code) took 38, 40 and 80 us at 64, at 64 with
-// all loads ahead, and at 2048.  The keys' bytes (D + 4 per token) bound it from
+// keys in blocks of 64 tokens take 30.2 us, in blocks of 128 or 256 28.6, of 16
+// 43.6, of 2048 127 (64 blocks a sequence leave most SMs idle; with one chain a
+// lane, whose bound puts every dim in doubt there, 230); sums in 64 bits
+// throughout (two more integer instructions a code) took 38 us at 64 and 105 at
+// 2048.  The keys' bytes (D + 4 per token) bound it from
 // below; the decoding of the codes, some ten instructions a token and warp,
 // comes close.
 #include <type_traits>
@@ -49,6 +51,7 @@ block_keys_kernel(const uint8_t *__restrict__ k_cache, const float *__restrict__
                   int64_t per_seq, int64_t total, int block, uint8_t *__restrict__ blk_cache,
                   float *__restrict__ blk_scale, int64_t n_max) {
     constexpr int kLanes = D / 16, kTok = 32 / kLanes, kOwn = D / 32;
+    __shared__ float2 total_sm[kWarps][8][32];
     const int lane = threadIdx.x & 31, piece = lane % kLanes, sub = lane / kLanes;
     const int64_t i = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (i >= total) return;
@@ -59,12 +62,13 @@ block_keys_kernel(const uint8_t *__restrict__ k_cache, const float *__restrict__
     float2 acc[8];
 #pragma unroll
     for (int d = 0; d < 8; d++) acc[d] = make_float2(0.f, 0.f);
-    // of the scales: the sum, and the sum of the partial sums (the error's bound)
-    float sum_s = 0.f, sum_p = 0.f;
+    // of the scales: the sum of the chains before, this chain's, and the sum of all
+    // partial sums (the error's bound)
+    float sum_s = 0.f, sum_b = 0.f, sum_p = 0.f;
     auto add = [&](const uint4 &w, float s) {
         const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-        sum_s += fabsf(s);
-        sum_p += sum_s;
+        sum_b += fabsf(s);
+        sum_p += sum_b;
 #pragma unroll
         for (int q = 0; q < 4; q++) {
             float f[4];
@@ -87,11 +91,32 @@ block_keys_kernel(const uint8_t *__restrict__ k_cache, const float *__restrict__
             }
 #pragma unroll
             for (int u = 0; u < kN; u++) add(w[u], s[u]);
+            if (kN == 16 && j + kTok * kN < block) {
+                // chains of sixteen, and a sum of them, in shared memory
+                sum_s += sum_b;
+                sum_p += sum_s;
+                sum_b = 0.f;
+#pragma unroll
+                for (int d = 0; d < 8; d++) {
+                    float2 &t = total_sm[threadIdx.x >> 5][d][lane];
+                    t = j == sub ? acc[d] : make_float2(t.x + acc[d].x, t.y + acc[d].y);
+                    acc[d] = make_float2(0.f, 0.f);
+                }
+            }
         }
     };
     batch(std::integral_constant<int, 16>());
     batch(std::integral_constant<int, 4>());
     batch(std::integral_constant<int, 1>());
+    if (sub + 16 * kTok < block) {
+        sum_p += sum_s + sum_b;
+#pragma unroll
+        for (int d = 0; d < 8; d++) {
+            const float2 t = total_sm[threadIdx.x >> 5][d][lane];
+            acc[d] = make_float2(t.x + acc[d].x, t.y + acc[d].y);
+        }
+    }
+    sum_s += sum_b;
     __syncwarp();
     // trade halves: the lane whose bit is set keeps the upper half of its dims
     float v[16];
@@ -122,8 +147,8 @@ block_keys_kernel(const uint8_t *__restrict__ k_cache, const float *__restrict__
     }
     amax = warp_max(amax);
     // How far the fp32 means may be off.  A term is at most 448 of its scale, so a
-    // lane's partial sums are at most 448 of its scales' partial sums, and each step
-    // is off by 2^-24 of one; a trade by 2^-24 of the sum so far, as are the two
+    // chain's partial sums are at most 448 of its scales' partial sums, and each step
+    // is off by 2^-24 of one, the sum of the chains' too; a trade by 2^-24 of the sum so far, as are the two
     // roundings of the mean.  (A sixteenth more for the roundings of the bound.)
     constexpr int kTrades = kTok == 8 ? 3 : 2;
     float err = sum_p + (kTrades + 2) * sum_s;
